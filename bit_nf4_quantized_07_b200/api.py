@@ -28,7 +28,8 @@ OP_DOUBLE_QUANT, OP_LINEAR_FWD, OP_LINEAR_BWD, OP_QUANTIZE_DQ_BATCH = 1, 2, 3, 4
 EXPORTS = ("nf4_quantize", "nf4_quantize_ex", "nf4_quantize_dq", "nf4_quantize_dq_batch", "nf4_double_quant", "nf4_double_quant_ex", "nf4_double_quant_noalloc",
            "nf4_dequant",
            "nf4_dequant_flat", "qlora_linear_fwd", "qlora_linear_bwd", "qln_workspace_bytes", "qln_codebook",
-           "qln_status_str", "qln_version", "qln_launch_count", "qln_adamw_step")
+           "qln_status_str", "qln_version", "qln_launch_count", "qln_adamw_step", "qln_adamw_multi_step",
+           "qln_adamw8_multi_step")
 DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
 DQ_FORMATS = {"int8": 0, "e4m3": 1}
 
@@ -45,6 +46,18 @@ class CAdamWConfig(ctypes.Structure):
 
 
 ADAMW_PAGE_IN, ADAMW_PAGE_OUT = 1, 2
+ADAMW8_BLOCK = 256  # elements that share a scale of an 8-bit state
+
+
+class CAdamWTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("param_bf16", ctypes.c_void_p), ("n", ctypes.c_int64)]
+
+
+class CAdamW8Tensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("param_bf16", ctypes.c_void_p), ("n", ctypes.c_int64)]
 
 
 class CQuantJob(ctypes.Structure):
@@ -89,6 +102,8 @@ def lib():
             "qln_version": ([], I32),
             "qln_launch_count": ([], ctypes.c_uint64),
             "qln_adamw_step": ([P, P, P, P, P, I64, ctypes.POINTER(CAdamWConfig), P, I32, P], I32),
+            "qln_adamw_multi_step": ([P, I32, ctypes.POINTER(CAdamWConfig), P, I32, P], I32),
+            "qln_adamw8_multi_step": ([P, I32, ctypes.POINTER(CAdamWConfig), P, I32, P], I32),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -115,6 +130,18 @@ def _need_cuda(*ts):
     for t in ts:
         if t is not None and (not t.is_cuda or not t.is_contiguous()):
             raise ValueError("tensors must be contiguous CUDA tensors")
+
+
+def _need_current(device, *ts):
+    """Contiguous CUDA tensors of `device`, which is the current one: the call
+    goes to the current device's current stream."""
+    if device.type != "cuda":
+        raise ValueError("tensors must be contiguous CUDA tensors")
+    for t in ts:
+        if t is not None and (t.device != device or not t.is_contiguous()):
+            raise ValueError("tensors must be contiguous CUDA tensors of one device")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
 
 
 def version() -> int:
@@ -396,3 +423,115 @@ def adamw_step(param: torch.Tensor, grad: torch.Tensor, m: torch.Tensor, v: torc
     cfg = CAdamWConfig(lr, betas[0], betas[1], eps, weight_decay)
     _check("qln_adamw_step", lib().qln_adamw_step(_p(param), _p(grad), _p(m), _p(v), _p(param_bf16), n,
                                                   ctypes.byref(cfg), _p(step), flags, _stream()))
+
+
+class _TensorList:
+    """The tensors of a list update, checked once, and their C descriptors.
+
+    Keeps the tensors alive; the update works on their memory as it is then, so
+    gradients are written into the same tensors before each step."""
+    _ctype = None
+
+    def __init__(self, count, fields):
+        # fields: name -> (list of tensors or None, allowed dtypes, elements for n elements of param)
+        if count < 1:
+            raise ValueError("the list of tensors is empty")
+        params = fields["param"][0]
+        self.device = params[0].device
+        self.tensors = {}
+        self.count = count
+        self.array = (self._ctype * count)()
+        spans = []  # (first byte, end, written)
+        for name, (ts, dtypes, size) in fields.items():
+            if ts is None:
+                continue
+            ts = list(ts)
+            if len(ts) != count:
+                raise ValueError(f"{len(ts)} {name} tensors for {count} parameters")
+            self.tensors[name] = ts
+            for i, t in enumerate(ts):
+                if t is None and name == "param_bf16":
+                    continue
+                n = params[i].numel()
+                if n < 1:
+                    raise ValueError(f"tensor {i}: a parameter is empty")
+                if t.dtype not in dtypes:
+                    raise ValueError(f"tensor {i}: {name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+                if t.numel() != size(n):
+                    raise ValueError(f"tensor {i}: {name} holds {t.numel()} elements, needs {size(n)}")
+                if not t.is_contiguous():
+                    raise ValueError(f"tensor {i}: {name} must be contiguous")
+                if t.device != self.device:
+                    raise ValueError(f"tensor {i}: {name} is on {t.device}, the first parameter on {self.device}")
+                setattr(self.array[i], name, t.data_ptr())
+                self.array[i].n = n
+                spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), name != "grad"))
+        spans.sort()
+        end, end_written = 0, False  # the furthest end so far, and whether a written buffer reaches it
+        for a, b, written in spans:
+            if a < end and (written or end_written):
+                raise ValueError("two of the list's buffers overlap")
+            if b > end:
+                end, end_written = b, written
+            elif b == end:
+                end_written = end_written or written
+
+
+class AdamWTensors(_TensorList):
+    """Parameters with 32-bit AdamW states for adamw_multi_step: lists of fp32
+    params, grads, m and v of equal sizes, and their BF16 copies (None, or a
+    list with None where a parameter has none)."""
+    _ctype = CAdamWTensor
+
+    def __init__(self, params, grads, m, v, params_bf16=None):
+        params = list(params)
+        f32, same = (torch.float32,), lambda n: n
+        super().__init__(len(params), {"param": (params, f32, same), "grad": (grads, f32, same), "m": (m, f32, same),
+                                       "v": (v, f32, same), "param_bf16": (params_bf16, (torch.bfloat16,), same)})
+
+
+class AdamW8Tensors(_TensorList):
+    """Parameters with 8-bit AdamW states for adamw8_multi_step: as AdamWTensors,
+    with m and v as E4M3 codes (float8_e4m3fn or uint8; v holds sqrt(v)) and
+    one fp32 scale per block of 256 elements (adamw8_state makes them)."""
+    _ctype = CAdamW8Tensor
+
+    def __init__(self, params, grads, m, m_scale, v, v_scale, params_bf16=None):
+        params = list(params)
+        f32, same = (torch.float32,), lambda n: n
+        e4m3, blocks = (torch.float8_e4m3fn, torch.uint8), lambda n: -(-n // ADAMW8_BLOCK)
+        super().__init__(len(params), {"param": (params, f32, same), "grad": (grads, f32, same), "m": (m, e4m3, same),
+                                       "m_scale": (m_scale, f32, blocks), "v": (v, e4m3, same),
+                                       "v_scale": (v_scale, f32, blocks),
+                                       "param_bf16": (params_bf16, (torch.bfloat16,), same)})
+
+
+def adamw8_state(param: torch.Tensor):
+    """(m, m_scale, v, v_scale) of a parameter before its first step."""
+    n, dev = param.numel(), param.device
+    nblk = -(-n // ADAMW8_BLOCK)
+    return (torch.zeros(n, dtype=torch.float8_e4m3fn, device=dev), torch.zeros(nblk, device=dev),
+            torch.zeros(n, dtype=torch.float8_e4m3fn, device=dev), torch.zeros(nblk, device=dev))
+
+
+def _multi_step(fn, tensors, cls, step, lr, betas, eps, weight_decay, flags):
+    if not isinstance(tensors, cls):
+        raise ValueError(f"tensors must be {cls.__name__}, got {type(tensors).__name__}")
+    if step.dtype != torch.int64 or step.numel() < 1:
+        raise ValueError("step must be an int64 tensor holding the step number")
+    _need_current(tensors.device, step)
+    cfg = CAdamWConfig(lr, betas[0], betas[1], eps, weight_decay)
+    _check(fn, getattr(lib(), fn)(tensors.array, tensors.count, ctypes.byref(cfg), _p(step), flags, _stream()))
+
+
+def adamw_multi_step(tensors: AdamWTensors, step: torch.Tensor, lr: float, betas=(0.9, 0.999), eps: float = 1e-8,
+                     weight_decay: float = 0.0, flags: int = 0):
+    """adamw_step of every tensor of the list in place, in one call
+    (qln_adamw_multi_step)."""
+    _multi_step("qln_adamw_multi_step", tensors, AdamWTensors, step, lr, betas, eps, weight_decay, flags)
+
+
+def adamw8_multi_step(tensors: AdamW8Tensors, step: torch.Tensor, lr: float, betas=(0.9, 0.999), eps: float = 1e-8,
+                      weight_decay: float = 0.0, flags: int = 0):
+    """adamw_multi_step with 8-bit states (qln_adamw8_multi_step)."""
+    _multi_step("qln_adamw8_multi_step", tensors, AdamW8Tensors, step, lr, betas, eps, weight_decay, flags)

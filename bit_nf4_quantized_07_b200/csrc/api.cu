@@ -20,6 +20,8 @@ using qln::note_launch;
 
 constexpr int kMaxDevices = 64;
 constexpr int32_t kMaxBatchJobs = 1 << 20;  // jobs per nf4_quantize_dq_batch call
+constexpr int32_t kMaxAdamwTensors = 1 << 20;       // tensors per list update
+constexpr int64_t kMaxAdamwElems = (int64_t)1 << 32;  // elements of one of its tensors
 int g_arch_ok[kMaxDevices];  // 0 unknown, 1 ok, -1 not sm_100
 int g_num_sms[kMaxDevices];
 
@@ -119,6 +121,35 @@ qln_status check_linear(const qln_nf4_weight *w, const uint16_t *X, int64_t n, c
 }
 
 qln_status from_cuda(cudaError_t e) { return e == cudaSuccess ? QLN_OK : QLN_ERR_CUDA; }
+
+qln_status check_adamw_tensor(const qln_adamw_tensor &t) {
+    if (!t.param || !t.grad || !t.m || !t.v) return QLN_ERR_NULL;
+    if (t.n <= 0 || t.n > kMaxAdamwElems) return QLN_ERR_SHAPE;
+    if (!aligned(t.param, 16) || !aligned(t.grad, 16) || !aligned(t.m, 16) || !aligned(t.v, 16)) return QLN_ERR_ALIGN;
+    return t.param_bf16 && !aligned(t.param_bf16, 8) ? QLN_ERR_ALIGN : QLN_OK;
+}
+
+qln_status check_adamw_tensor(const qln_adamw8_tensor &t) {
+    if (!t.param || !t.grad || !t.m || !t.m_scale || !t.v || !t.v_scale) return QLN_ERR_NULL;
+    if (t.n <= 0 || t.n > kMaxAdamwElems) return QLN_ERR_SHAPE;
+    if (!aligned(t.param, 16) || !aligned(t.grad, 16) || !aligned(t.m, 8) || !aligned(t.v, 8) ||
+        !aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))
+        return QLN_ERR_ALIGN;
+    return t.param_bf16 && !aligned(t.param_bf16, 16) ? QLN_ERR_ALIGN : QLN_OK;
+}
+
+// The checks that both list updates share; *num_sms of the current device.
+template <typename Tensor>
+qln_status check_adamw_list(const Tensor *tensors, int32_t count, const qln_adamw_config *cfg,
+                                   const int64_t *step, int *num_sms) {
+    if (!tensors || !cfg || !step) return QLN_ERR_NULL;
+    if (count < 1 || count > kMaxAdamwTensors) return QLN_ERR_SHAPE;
+    for (int32_t i = 0; i < count; ++i) {
+        const qln_status s = check_adamw_tensor(tensors[i]);
+        if (s != QLN_OK) return s;
+    }
+    return check_device(num_sms);
+}
 
 // The fused weight GEMM: tcgen05 where the shape fills its tiles, otherwise
 // the register-level path.
@@ -269,6 +300,22 @@ qln_status qln_adamw_step(float *param, const float *grad, float *m, float *v, u
     if (s != QLN_OK) return s;
     return from_cuda(qln::launch_adamw(param, grad, m, v, param_bf16, n, cfg->lr, cfg->beta1, cfg->beta2, cfg->eps,
                                        cfg->weight_decay, step, flags, (cudaStream_t)stream, sms));
+}
+
+qln_status qln_adamw_multi_step(const qln_adamw_tensor *tensors, int32_t count, const qln_adamw_config *cfg,
+                                const int64_t *step, int32_t flags, void *stream) {
+    int sms = 0;
+    const qln_status s = check_adamw_list(tensors, count, cfg, step, &sms);
+    if (s != QLN_OK) return s;
+    return from_cuda(qln::launch_adamw_multi(tensors, count, cfg, step, flags, (cudaStream_t)stream, sms));
+}
+
+qln_status qln_adamw8_multi_step(const qln_adamw8_tensor *tensors, int32_t count, const qln_adamw_config *cfg,
+                                 const int64_t *step, int32_t flags, void *stream) {
+    int sms = 0;
+    const qln_status s = check_adamw_list(tensors, count, cfg, step, &sms);
+    if (s != QLN_OK) return s;
+    return from_cuda(qln::launch_adamw8_multi(tensors, count, cfg, step, flags, (cudaStream_t)stream, sms));
 }
 
 qln_status nf4_dequant_flat(const qln_nf4_weight *w, int64_t numel, uint16_t *out, void *stream) {

@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(256) adamw_kernel(const AdamWArgs a) {
 
 // Managed-memory pages of [ptr, ptr + bytes) to `device` (cudaCpuDeviceId for
 // host RAM), queued on the stream; nothing for memory of any other kind.
-static cudaError_t page_to(const void *ptr, size_t bytes, int device, cudaStream_t st) {
+cudaError_t page_managed(const void *ptr, size_t bytes, int device, cudaStream_t st) {
     cudaPointerAttributes at;
     cudaError_t e = cudaPointerGetAttributes(&at, ptr);
     if (e != cudaSuccess) {
@@ -101,7 +101,7 @@ cudaError_t launch_adamw(float *p, const float *g, float *m, float *v, uint16_t 
     if (flags & QLN_ADAMW_PAGE_IN) {  // page the operands back in before the update
         const void *ops[4] = {p, g, m, v};
         for (const void *q : ops)
-            if ((e = page_to(q, bytes, dev, st)) != cudaSuccess) return e;
+            if ((e = page_managed(q, bytes, dev, st)) != cudaSuccess) return e;
     }
     AdamWArgs a{p, g, m, v, p_bf16, n, lr, b1, b2, eps, wd, step};
     int64_t grid = (n / 4 + 255) / 256;
@@ -110,8 +110,8 @@ cudaError_t launch_adamw(float *p, const float *g, float *m, float *v, uint16_t 
     e = launch_pdl(adamw_kernel, dim3((unsigned)grid), dim3(256), 0, st, a);
     if (e != cudaSuccess) return e;
     if (flags & QLN_ADAMW_PAGE_OUT) {  // states back to host RAM until the next update
-        if ((e = page_to(m, bytes, cudaCpuDeviceId, st)) != cudaSuccess) return e;
-        if ((e = page_to(v, bytes, cudaCpuDeviceId, st)) != cudaSuccess) return e;
+        if ((e = page_managed(m, bytes, cudaCpuDeviceId, st)) != cudaSuccess) return e;
+        if ((e = page_managed(v, bytes, cudaCpuDeviceId, st)) != cudaSuccess) return e;
     }
     return cudaSuccess;
 }

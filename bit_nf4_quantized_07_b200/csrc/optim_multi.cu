@@ -1,0 +1,340 @@
+// One AdamW update over a list of tensors, with 32-bit or 8-bit states: the
+// optimizer step of many LoRA factors in one call.
+//
+// Pages: deck "3 QLoRA Finetuning" cards 1 and 5 (only the adapters are
+// updated; paged optimizer states); "LoRA 与 QLoRA" QLoRA usage notes (the
+// paged AdamW of the adapter parameters).  The update is the published AdamW
+// (Loshchilov & Hutter, "Decoupled Weight Decay Regularization", ICLR 2019),
+// decay first:
+//   m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2;  p = p (1 - lr wd);
+//   p = p - (lr / (1 - b1^t)) m / (sqrt(v / (1 - b2^t)) + eps)
+//
+// 8-bit states.  Blocks of 256 consecutive elements of a tensor share one fp32
+// scale b = max|x| / 448 and hold E4M3 codes of x / b, the group format that
+// the double quantization uses for the block constants.  The first moment is
+// held as x = m, the second as x = sqrt(v): its square spans 2^36 within a
+// block instead of 2^18.  A nonzero sqrt(v) is never rounded to zero (it takes
+// the smallest code): a zero denominator under a nonzero m would turn the step
+// into lr m / eps.  The update itself runs in fp32 on the restored states, and
+// uses the new v before it is rounded.
+//
+// Both kernels are HBM-bound.  The tensors' pointers travel as a kernel
+// parameter (up to 32 KB), so nothing is copied or allocated and a captured
+// launch holds its own table.  A tensor is cut into chunks of 2048 elements;
+// CTA i takes an equal contiguous share of all chunks, finds its first tensor
+// by bisection and walks on from there.
+#include "qln_common.cuh"
+#include "qln_internal.h"
+
+namespace qln {
+
+constexpr int kMtChunk = 2048;   // elements per CTA step: 256 threads x 8
+constexpr int kMtThreads = 256;
+constexpr int kBlock8 = QLN_ADAMW8_BLOCK;
+constexpr float kE4m3Max = 448.f;
+
+// Tensors per launch: the table and its arguments stay within the 32,764
+// bytes of a launch's parameters.
+constexpr int kMtMax = 480;
+struct MtArgs {
+    float lr, b1, b2, eps, wd;
+    const int64_t *step;
+    int count;
+    uint32_t chunk0[kMtMax + 1];  // first chunk of each tensor; [count] = all chunks
+};
+struct Mt32Table {
+    MtArgs a;
+    qln_adamw_tensor t[kMtMax];
+};
+struct Mt8Table {
+    MtArgs a;
+    qln_adamw8_tensor t[kMtMax];
+};
+static_assert(sizeof(Mt32Table) <= 32764 && sizeof(Mt8Table) <= 32764, "kernel parameter limit");
+
+// b^t by squaring (t >= 1), binary64: relative error about t 2^-53 while b^t
+// is not negligible against 1.
+__device__ __forceinline__ double pow_int(double b, int64_t t) {
+    double r = 1.0;
+    for (; t > 0; t >>= 1) {
+        if (t & 1) r *= b;
+        b *= b;
+        if (b == 0.0 && t > 1) return 0.0;
+    }
+    return r;
+}
+
+struct MtStep {
+    float step_size, inv_sqrt_bc2;
+};
+
+// The step's two factors, formed by one thread of the CTA.
+__device__ __forceinline__ MtStep mt_step(const MtArgs &a) {
+    const int64_t tv = *a.step;
+    const int64_t t = tv < 1 ? 1 : tv;  // a step below 1 is taken as the first
+    MtStep s;
+    s.step_size = (float)((double)a.lr / (1.0 - pow_int((double)a.b1, t)));
+    s.inv_sqrt_bc2 = (float)(1.0 / sqrt(1.0 - pow_int((double)a.b2, t)));
+    return s;
+}
+
+// One element in fp32; returns sqrt(v).
+__device__ __forceinline__ float mt_elem(float &p, float g, float &m, float &v, const MtArgs &a, const MtStep &s) {
+    m = __fadd_rn(__fmul_rn(a.b1, m), __fmul_rn(1.0f - a.b1, g));
+    v = __fadd_rn(__fmul_rn(a.b2, v), __fmul_rn(1.0f - a.b2, __fmul_rn(g, g)));
+    p = __fmul_rn(p, 1.0f - a.lr * a.wd);
+    const float rv = __fsqrt_rn(v);
+    const float denom = __fadd_rn(__fmul_rn(rv, s.inv_sqrt_bc2), a.eps);
+    p = __fsub_rn(p, __fmul_rn(s.step_size, __fdiv_rn(m, denom)));
+    return rv;
+}
+
+// The CTA's share of the chunks and the tensor its first chunk lies in.
+struct MtRange {
+    uint32_t c, end;
+    int ti;
+};
+__device__ __forceinline__ MtRange mt_range(const MtArgs &a) {
+    const uint64_t total = a.chunk0[a.count];
+    MtRange r;
+    r.c = (uint32_t)(total * blockIdx.x / gridDim.x);
+    r.end = (uint32_t)(total * (blockIdx.x + 1) / gridDim.x);
+    int lo = 0, hi = a.count;  // chunk0[lo] <= c < chunk0[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.chunk0[mid] <= r.c) lo = mid;
+        else hi = mid;
+    }
+    r.ti = lo;
+    return r;
+}
+
+__global__ void __launch_bounds__(kMtThreads) adamw_multi_kernel(const __grid_constant__ Mt32Table T) {
+    __shared__ MtStep sh;
+    MtRange R = mt_range(T.a);
+    pdl_wait();
+    pdl_trigger();
+    if (threadIdx.x == 0) sh = mt_step(T.a);
+    __syncthreads();
+    const MtStep S = sh;
+    for (; R.c < R.end; ++R.c) {
+        while (R.c >= T.a.chunk0[R.ti + 1]) ++R.ti;
+        const qln_adamw_tensor &t = T.t[R.ti];
+        const int64_t e0 = (int64_t)(R.c - T.a.chunk0[R.ti]) * kMtChunk;
+        const int64_t left = t.n - e0;
+        if (left >= kMtChunk) {
+            float4 p[2], g[2], m[2], v[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int64_t i = (e0 >> 2) + u * kMtThreads + threadIdx.x;
+                g[u] = __ldcs(reinterpret_cast<const float4 *>(t.grad) + i);
+                m[u] = reinterpret_cast<const float4 *>(t.m)[i];
+                v[u] = reinterpret_cast<const float4 *>(t.v)[i];
+                p[u] = reinterpret_cast<const float4 *>(t.param)[i];
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int64_t i = (e0 >> 2) + u * kMtThreads + threadIdx.x;
+                mt_elem(p[u].x, g[u].x, m[u].x, v[u].x, T.a, S);
+                mt_elem(p[u].y, g[u].y, m[u].y, v[u].y, T.a, S);
+                mt_elem(p[u].z, g[u].z, m[u].z, v[u].z, T.a, S);
+                mt_elem(p[u].w, g[u].w, m[u].w, v[u].w, T.a, S);
+                reinterpret_cast<float4 *>(t.param)[i] = p[u];
+                reinterpret_cast<float4 *>(t.m)[i] = m[u];
+                reinterpret_cast<float4 *>(t.v)[i] = v[u];
+                if (t.param_bf16)
+                    reinterpret_cast<uint2 *>(t.param_bf16)[i] =
+                        make_uint2(pack_bf16x2(p[u].x, p[u].y), pack_bf16x2(p[u].z, p[u].w));
+            }
+        } else {  // a tensor's last chunk: element by element
+            for (int64_t i = e0 + threadIdx.x; i < t.n; i += kMtThreads) {
+                float p = t.param[i], m = t.m[i], v = t.v[i];
+                mt_elem(p, t.grad[i], m, v, T.a, S);
+                t.param[i] = p;
+                t.m[i] = m;
+                t.v[i] = v;
+                if (t.param_bf16) t.param_bf16[i] = __bfloat16_as_ushort(__float2bfloat16_rn(p));
+            }
+        }
+    }
+}
+
+// ---- 8-bit states ------------------------------------------------------------
+// Four codes of one word -> fp32, times the block's scale.
+__device__ __forceinline__ void e4m3x4_restore(uint32_t w, float b, float *x) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((w >> (16 * h)) & 0xffffu), __NV_E4M3);
+        const float2 f = __half22float2(__half2(r));
+        x[2 * h] = __fmul_rn(f.x, b);
+        x[2 * h + 1] = __fmul_rn(f.y, b);
+    }
+}
+// Four values already divided by the scale -> codes (round to nearest even;
+// NaN stays NaN).
+__device__ __forceinline__ uint32_t e4m3x4_pack(const float *y) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+// |x| as ordered bits; 0 for infinities and NaN, which set no scale.
+__device__ __forceinline__ uint32_t abs_bits_finite(float x) {
+    const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
+    return b < 0x7f800000u ? b : 0u;
+}
+// x / b for the code; a non-finite element becomes NaN, so that it stays an
+// element's own fault instead of a saturated value.
+__device__ __forceinline__ float scaled(float x, float b) {
+    const float y = b > 0.f ? __fdiv_rn(x, b) : 0.f;
+    return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u ? __uint_as_float(0x7fffffffu) : y;
+}
+
+__global__ void __launch_bounds__(kMtThreads) adamw8_multi_kernel(const __grid_constant__ Mt8Table T) {
+    static_assert(kBlock8 == 256 && kMtChunk == 8 * kBlock8, "one block per warp and step");
+    __shared__ MtStep sh;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    MtRange R = mt_range(T.a);
+    pdl_wait();
+    pdl_trigger();
+    if (threadIdx.x == 0) sh = mt_step(T.a);
+    __syncthreads();
+    const MtStep S = sh;
+    for (; R.c < R.end; ++R.c) {
+        while (R.c >= T.a.chunk0[R.ti + 1]) ++R.ti;
+        const qln_adamw8_tensor &t = T.t[R.ti];
+        const int64_t blk = (int64_t)(R.c - T.a.chunk0[R.ti]) * (kMtChunk / kBlock8) + warp;
+        const int64_t e = blk * kBlock8 + 8 * lane;  // this lane's 8 elements
+        if (blk * kBlock8 >= t.n) continue;
+        const int64_t left = t.n - e;
+        const bool full = left >= 8;
+        const float bm = t.m_scale[blk], bv = t.v_scale[blk];
+        float p[8], g[8], m[8], v[8];
+        if (full) {
+            const uint2 mc = *reinterpret_cast<const uint2 *>(t.m + e);
+            const uint2 vc = *reinterpret_cast<const uint2 *>(t.v + e);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float4 g4 = __ldcs(reinterpret_cast<const float4 *>(t.grad + e) + h);
+                const float4 p4 = *(reinterpret_cast<const float4 *>(t.param + e) + h);
+                g[4 * h] = g4.x, g[4 * h + 1] = g4.y, g[4 * h + 2] = g4.z, g[4 * h + 3] = g4.w;
+                p[4 * h] = p4.x, p[4 * h + 1] = p4.y, p[4 * h + 2] = p4.z, p[4 * h + 3] = p4.w;
+            }
+            e4m3x4_restore(mc.x, bm, m);
+            e4m3x4_restore(mc.y, bm, m + 4);
+            e4m3x4_restore(vc.x, bv, v);
+            e4m3x4_restore(vc.y, bv, v + 4);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const bool in = k < left;
+                g[k] = in ? t.grad[e + k] : 0.f;
+                p[k] = in ? t.param[e + k] : 0.f;
+                m[k] = in ? __fmul_rn(e4m3_to_f32(t.m[e + k]), bm) : 0.f;
+                v[k] = in ? __fmul_rn(e4m3_to_f32(t.v[e + k]), bv) : 0.f;
+            }
+        }
+        uint32_t am = 0, av = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            v[k] = __fmul_rn(v[k], v[k]);
+            v[k] = mt_elem(p[k], g[k], m[k], v[k], T.a, S);  // now sqrt(v)
+            am = max(am, abs_bits_finite(m[k]));
+            av = max(av, abs_bits_finite(v[k]));
+        }
+        am = __reduce_max_sync(0xffffffffu, am);
+        av = __reduce_max_sync(0xffffffffu, av);
+        const float nm = __fdiv_rn(__uint_as_float(am), kE4m3Max), nv = __fdiv_rn(__uint_as_float(av), kE4m3Max);
+        float ym[8], yv[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            ym[k] = scaled(m[k], nm);
+            yv[k] = scaled(v[k], nv);
+            if (v[k] > 0.f && yv[k] < 0.001953125f) yv[k] = 0.001953125f;  // 2^-9, the smallest code
+        }
+        const uint2 mo = make_uint2(e4m3x4_pack(ym), e4m3x4_pack(ym + 4));
+        const uint2 vo = make_uint2(e4m3x4_pack(yv), e4m3x4_pack(yv + 4));
+        if (lane == 0) {
+            t.m_scale[blk] = nm;
+            t.v_scale[blk] = nv;
+        }
+        if (full) {
+            *reinterpret_cast<uint2 *>(t.m + e) = mo;
+            *reinterpret_cast<uint2 *>(t.v + e) = vo;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                *(reinterpret_cast<float4 *>(t.param + e) + h) = make_float4(p[4 * h], p[4 * h + 1], p[4 * h + 2], p[4 * h + 3]);
+            if (t.param_bf16)
+                *reinterpret_cast<uint4 *>(t.param_bf16 + e) =
+                    make_uint4(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]), pack_bf16x2(p[4], p[5]), pack_bf16x2(p[6], p[7]));
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < left) {
+                    t.param[e + k] = p[k];
+                    t.m[e + k] = (uint8_t)((k < 4 ? mo.x : mo.y) >> (8 * (k & 3)));
+                    t.v[e + k] = (uint8_t)((k < 4 ? vo.x : vo.y) >> (8 * (k & 3)));
+                    if (t.param_bf16) t.param_bf16[e + k] = __bfloat16_as_ushort(__float2bfloat16_rn(p[k]));
+                }
+        }
+    }
+}
+
+// ---- host ----------------------------------------------------------------------
+static cudaError_t page_tensor(const qln_adamw_tensor &t, bool in, int dev, cudaStream_t st) {
+    const size_t b = (size_t)t.n * 4;
+    cudaError_t e;
+    if (in && ((e = page_managed(t.param, b, dev, st)) != cudaSuccess || (e = page_managed(t.grad, b, dev, st)) != cudaSuccess)) return e;
+    if ((e = page_managed(t.m, b, dev, st)) != cudaSuccess) return e;
+    return page_managed(t.v, b, dev, st);
+}
+static cudaError_t page_tensor(const qln_adamw8_tensor &t, bool in, int dev, cudaStream_t st) {
+    const size_t b = (size_t)t.n, s = (size_t)((t.n + kBlock8 - 1) / kBlock8) * 4;
+    cudaError_t e;
+    if (in && ((e = page_managed(t.param, 4 * b, dev, st)) != cudaSuccess || (e = page_managed(t.grad, 4 * b, dev, st)) != cudaSuccess)) return e;
+    if ((e = page_managed(t.m, b, dev, st)) != cudaSuccess || (e = page_managed(t.v, b, dev, st)) != cudaSuccess) return e;
+    if ((e = page_managed(t.m_scale, s, dev, st)) != cudaSuccess) return e;
+    return page_managed(t.v_scale, s, dev, st);
+}
+
+template <typename Table, typename Tensor>
+static cudaError_t launch_multi(void (*kernel)(const Table), const Tensor *tensors, int count, const qln_adamw_config *cfg,
+                                const int64_t *step, int flags, cudaStream_t st, int num_sms) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (flags & QLN_ADAMW_PAGE_IN)
+        for (int i = 0; i < count; ++i)
+            if ((e = page_tensor(tensors[i], true, dev, st)) != cudaSuccess) return e;
+    Table T;
+    T.a.lr = cfg->lr, T.a.b1 = cfg->beta1, T.a.b2 = cfg->beta2, T.a.eps = cfg->eps, T.a.wd = cfg->weight_decay;
+    T.a.step = step;
+    for (int i0 = 0; i0 < count; i0 += T.a.count) {
+        const int k = count - i0 < kMtMax ? count - i0 : kMtMax;
+        uint64_t chunks = 0;
+        T.a.count = k;
+        for (int i = 0; i < k; ++i) {
+            T.a.chunk0[i] = (uint32_t)chunks;
+            T.t[i] = tensors[i0 + i];
+            chunks += (uint64_t)(tensors[i0 + i].n + kMtChunk - 1) / kMtChunk;
+        }
+        T.a.chunk0[k] = (uint32_t)chunks;
+        const uint64_t wave = (uint64_t)num_sms * 4;
+        e = launch_pdl(kernel, dim3((unsigned)(chunks < wave ? chunks : wave)), dim3(kMtThreads), 0, st, T);
+        if (e != cudaSuccess) return e;
+    }
+    if (flags & QLN_ADAMW_PAGE_OUT)
+        for (int i = 0; i < count; ++i)
+            if ((e = page_tensor(tensors[i], false, cudaCpuDeviceId, st)) != cudaSuccess) return e;
+    return cudaSuccess;
+}
+
+cudaError_t launch_adamw_multi(const qln_adamw_tensor *t, int count, const qln_adamw_config *cfg, const int64_t *step,
+                               int flags, cudaStream_t st, int num_sms) {
+    return launch_multi<Mt32Table>(adamw_multi_kernel, t, count, cfg, step, flags, st, num_sms);
+}
+cudaError_t launch_adamw8_multi(const qln_adamw8_tensor *t, int count, const qln_adamw_config *cfg, const int64_t *step,
+                                int flags, cudaStream_t st, int num_sms) {
+    return launch_multi<Mt8Table>(adamw8_multi_kernel, t, count, cfg, step, flags, st, num_sms);
+}
+
+}  // namespace qln

@@ -61,6 +61,14 @@ cudaError_t launch_nf4_dequant(const qln_nf4_weight *w, uint16_t *out, cudaStrea
 cudaError_t launch_adamw(float *p, const float *g, float *m, float *v, uint16_t *p_bf16, int64_t n, float lr,
                          float b1, float b2, float eps, float wd, const int64_t *step, int flags, cudaStream_t st,
                          int num_sms);
+// optim.cu: the managed-memory pages of [ptr, ptr + bytes) to `device`
+// (cudaCpuDeviceId: host RAM) on the stream; nothing for other memory.
+cudaError_t page_managed(const void *ptr, size_t bytes, int device, cudaStream_t st);
+// optim_multi.cu: one AdamW update over a list of tensors (validated by the caller).
+cudaError_t launch_adamw_multi(const qln_adamw_tensor *t, int count, const qln_adamw_config *cfg, const int64_t *step,
+                               int flags, cudaStream_t st, int num_sms);
+cudaError_t launch_adamw8_multi(const qln_adamw8_tensor *t, int count, const qln_adamw_config *cfg, const int64_t *step,
+                                int flags, cudaStream_t st, int num_sms);
 cudaError_t launch_nf4_dequant_flat(const qln_nf4_weight *w, int64_t numel, uint16_t *out, cudaStream_t st,
                                     int num_sms);
 size_t dq_workspace_bytes(int64_t nb);

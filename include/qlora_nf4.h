@@ -406,6 +406,70 @@ QLN_API qln_status qln_adamw_step(float *param, const float *grad, float *m, flo
                                   int64_t n, const qln_adamw_config *cfg, const int64_t *step, int32_t flags,
                                   void *stream);
 
+/* One tensor of qln_adamw_multi_step: the pointers and size of qln_adamw_step. */
+typedef struct {
+    float *param;         /* [n] fp32 in/out                       */
+    const float *grad;    /* [n] fp32 in                           */
+    float *m;             /* [n] fp32 in/out                       */
+    float *v;             /* [n] fp32 in/out                       */
+    uint16_t *param_bf16; /* [n] bf16 out, or NULL                 */
+    int64_t n;            /* 1 .. 2^32                             */
+} qln_adamw_tensor;
+
+/*
+ * qln_adamw_multi_step -- qln_adamw_step of `count` tensors in one call: the
+ * optimizer step of all LoRA factors of a model, or of a pool of adapters.
+ * Defined by the passages that qln_adamw_step cites; the same update with the
+ * same hyper-parameters, step and flags for every tensor (to the rounding of
+ * the bias corrections, which are formed in binary64 here too).
+ *   tensors  HOST array of `count` descriptors, read during the call only (a
+ *            captured CUDA graph holds its own copy).  No tensor's param, m, v
+ *            or param_bf16 may overlap any other buffer of the list.
+ * One launch per 480 tensors.
+ * Errors: QLN_ERR_NULL (tensors, cfg, step, or a tensor's pointer);
+ * QLN_ERR_SHAPE (count < 1 or above 2^20, n out of range); QLN_ERR_ALIGN as
+ * qln_adamw_step.  Every tensor is checked before anything is launched.
+ */
+QLN_API qln_status qln_adamw_multi_step(const qln_adamw_tensor *tensors, int32_t count, const qln_adamw_config *cfg,
+                                        const int64_t *step, int32_t flags, void *stream);
+
+/* Elements of a tensor that share one scale of an 8-bit AdamW state. */
+enum { QLN_ADAMW8_BLOCK = 256 };
+
+/* One tensor of qln_adamw8_multi_step; nblk = ceil(n / 256). */
+typedef struct {
+    float *param;         /* [n] fp32 in/out                       */
+    const float *grad;    /* [n] fp32 in                           */
+    uint8_t *m;           /* [n] E4M3 codes in/out                 */
+    float *m_scale;       /* [nblk] fp32 in/out                    */
+    uint8_t *v;           /* [n] E4M3 codes of sqrt(v) in/out      */
+    float *v_scale;       /* [nblk] fp32 in/out                    */
+    uint16_t *param_bf16; /* [n] bf16 out, or NULL                 */
+    int64_t n;            /* 1 .. 2^32                             */
+} qln_adamw8_tensor;
+
+/*
+ * qln_adamw8_multi_step -- qln_adamw_multi_step with 8-bit states: 2 bytes and
+ * 1/32 byte of scales per parameter instead of 8.
+ * Defined by the passages that qln_adamw_step cites; the pages do not describe
+ * 8-bit states.  They are held in the library's 8-bit group format
+ * (QLN_DQ_E4M3, without the mean): the 256 elements of a block (the last block
+ * of a tensor may be partial) share b = fp32(max|x| / 448), and an element's
+ * code is E4M3(fp32(x / b)), round to nearest even, 0 when b == 0.  The first
+ * moment is held as x = m, the second as x = sqrt(v).  A sqrt(v) above zero
+ * never takes code 0: it is raised to the smallest code (2^-9).
+ * A step restores m = fp32(b code) and v = fp32(fp32(b code)^2), updates as
+ * qln_adamw_step in fp32, and stores the new states; the parameter's own step
+ * uses them before they are rounded.  Zero codes and zero scales are the
+ * states before step 1.  An infinite or NaN element (of m or sqrt(v)) sets no
+ * scale and is stored as NaN: it spoils its own parameter and no other.
+ * tensors, cfg, step, flags and errors as qln_adamw_multi_step; QLN_ERR_ALIGN
+ * if param or grad is not 16-byte aligned, m or v not 8-byte, a scale not
+ * 4-byte, or param_bf16 not 16-byte.
+ */
+QLN_API qln_status qln_adamw8_multi_step(const qln_adamw8_tensor *tensors, int32_t count, const qln_adamw_config *cfg,
+                                         const int64_t *step, int32_t flags, void *stream);
+
 /* Device workspace, in bytes, that `op` needs for these sizes (nb for
  * QLN_OP_DOUBLE_QUANT and the job count for QLN_OP_QUANTIZE_DQ_BATCH are
  * passed as `rows`).  Returns 0 for an unknown op. */
