@@ -22,14 +22,15 @@ LIB_PATH = os.path.join(_HERE, "libqlora_nf4.so")
 QLN_OK = 0
 STATUS_NAMES = {0: "QLN_OK", 1: "QLN_ERR_NULL", 2: "QLN_ERR_SHAPE", 3: "QLN_ERR_ALIGN", 4: "QLN_ERR_WORKSPACE",
                 5: "QLN_ERR_ARCH", 6: "QLN_ERR_CUDA", 7: "QLN_ERR_TIMEOUT", 8: "QLN_ERR_INTERNAL"}
-OP_DOUBLE_QUANT, OP_LINEAR_FWD, OP_LINEAR_BWD, OP_QUANTIZE_DQ_BATCH = 1, 2, 3, 4
+OP_DOUBLE_QUANT, OP_LINEAR_FWD, OP_LINEAR_BWD, OP_QUANTIZE_DQ_BATCH, OP_MULTI_FWD, OP_MULTI_BWD = 1, 2, 3, 4, 5, 6
+MAX_ADAPTERS = 1024  # adapters of one pool
 
 #: Every symbol include/qlora_nf4.h declares.
 EXPORTS = ("nf4_quantize", "nf4_quantize_ex", "nf4_quantize_dq", "nf4_quantize_dq_batch", "nf4_double_quant", "nf4_double_quant_ex", "nf4_double_quant_noalloc",
            "nf4_dequant",
            "nf4_dequant_flat", "qlora_linear_fwd", "qlora_linear_bwd", "qln_workspace_bytes", "qln_codebook",
            "qln_status_str", "qln_version", "qln_launch_count", "qln_adamw_step", "qln_adamw_multi_step",
-           "qln_adamw8_multi_step")
+           "qln_adamw8_multi_step", "qlora_multi_fwd", "qlora_multi_bwd")
 DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
 DQ_FORMATS = {"int8": 0, "e4m3": 1}
 
@@ -66,6 +67,11 @@ class CQuantJob(ctypes.Structure):
                 ("qabs", ctypes.c_void_p), ("dq_scale", ctypes.c_void_p), ("dq_mean", ctypes.c_void_p)]
 
 
+class CAdapterPool(ctypes.Structure):
+    _fields_ = [("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("rank", ctypes.c_void_p),
+                ("count", ctypes.c_int32), ("r", ctypes.c_int32)]
+
+
 class CNF4Weight(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("absmax", ctypes.c_void_p), ("qabs", ctypes.c_void_p),
                 ("dq_scale", ctypes.c_void_p), ("dq_mean", ctypes.c_void_p), ("rows", ctypes.c_int64),
@@ -83,7 +89,7 @@ def lib():
             raise RuntimeError(f"{LIB_PATH} is missing: build it with bit_nf4_quantized_07_b200.build.build()")
         L = ctypes.CDLL(LIB_PATH)
         P, I64, I32, SZ, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
-        WP = ctypes.POINTER(CNF4Weight)
+        WP, PP = ctypes.POINTER(CNF4Weight), ctypes.POINTER(CAdapterPool)
         sig = {
             "nf4_quantize": ([P, I64, P, P, P], I32),
             "nf4_quantize_ex": ([P, I32, I64, P, P, P], I32),
@@ -96,6 +102,8 @@ def lib():
             "nf4_dequant_flat": ([WP, I64, P, P], I32),
             "qlora_linear_fwd": ([WP, P, I64, P, P, I32, F, P, P, P, SZ, P], I32),
             "qlora_linear_bwd": ([WP, P, I64, P, P, I32, F, P, P, P, P, P, P, SZ, P], I32),
+            "qlora_multi_fwd": ([WP, PP, P, I64, P, P, P, P, SZ, P], I32),
+            "qlora_multi_bwd": ([WP, PP, P, I64, P, P, P, P, P, P, P, SZ, P], I32),
             "qln_workspace_bytes": ([I32, I64, I64, I64, I32], SZ),
             "qln_codebook": ([P], None),
             "qln_status_str": ([I32], ctypes.c_char_p),
@@ -405,6 +413,95 @@ def qlora_linear_bwd(w: NF4Weight, X, A, B, s: float, dY, U=None, dX=None, dA=No
     cw = w.c_struct()
     _check("qlora_linear_bwd", lib().qlora_linear_bwd(ctypes.byref(cw), _p(X), n, _p(A), _p(B), r, float(s), _p(dY),
                                                       _p(U), _p(dX), _p(dA), _p(dB), _p(ws), ws.numel(), _stream()))
+    return dX, dA, dB
+
+
+class AdapterPool:
+    """LoRA adapters over one weight, for the tokens of a batch to choose from.
+
+    A bf16 [count][r][din], B bf16 [count][dout][r], scale fp32 [count], and
+    rank int32 [count] or None (every adapter has rank r).  The tensors are
+    checked once and kept; their contents may change between calls."""
+
+    def __init__(self, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor, rank: Optional[torch.Tensor] = None):
+        if A.dim() != 3 or B.dim() != 3:
+            raise ValueError("A is [count][r][din] and B [count][dout][r]")
+        count, r, _ = A.shape
+        if B.shape[0] != count or B.shape[2] != r:
+            raise ValueError(f"A {tuple(A.shape)} and B {tuple(B.shape)} disagree on the count or the rank")
+        for name, t, dt in (("A", A, torch.bfloat16), ("B", B, torch.bfloat16), ("scale", scale, torch.float32),
+                            ("rank", rank, torch.int32)):
+            if t is None and name == "rank":
+                continue
+            if t.dtype != dt:
+                raise ValueError(f"{name} must be {dt}, got {t.dtype}")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+            if t.device != A.device:
+                raise ValueError(f"{name} is on {t.device}, A on {A.device}")
+            if name in ("scale", "rank") and t.numel() != count:
+                raise ValueError(f"{name} holds {t.numel()} elements, needs {count}")
+        self.A, self.B, self.scale, self.rank = A, B, scale, rank
+        self.count, self.r, self.din, self.dout, self.device = count, r, A.shape[2], B.shape[1], A.device
+        self.c = CAdapterPool(A.data_ptr(), B.data_ptr(), scale.data_ptr(), None if rank is None else rank.data_ptr(),
+                              count, r)
+
+
+def _check_multi(w: NF4Weight, pool: AdapterPool, X, ids, others):
+    """Shapes, types and device of a call with a pool (the library works on raw
+    pointers); others: (name, tensor or None, dtype, shape)."""
+    n = X.shape[0]
+    if (w.rows, w.cols) != (pool.dout, pool.din):
+        raise ValueError(f"the weight is {w.rows} x {w.cols}, the pool's adapters {pool.dout} x {pool.din}")
+    for name, t, dt, shape in (("X", X, torch.bfloat16, (n, w.cols)), ("ids", ids, torch.int32, (n,)), *others):
+        if t is not None and (t.dtype != dt or t.shape != shape):
+            raise ValueError(f"{name} must be {dt} {shape}, got {t.dtype} {tuple(t.shape)}")
+    _need_current(pool.device, X, ids, w.codes, w.absmax, w.qabs, w.dq_scale, w.dq_mean, *(o[1] for o in others))
+
+
+def _multi_workspace(op, w, n, r, ws, device):
+    """The call's scratch (it keeps no state, so it need not be zeroed)."""
+    if ws is None:
+        return torch.empty(workspace_bytes(op, w.rows, w.cols, n, r), dtype=torch.uint8, device=device)
+    _need_current(device, ws)
+    return ws
+
+
+def qlora_multi_fwd(w: NF4Weight, pool: AdapterPool, X, ids, Y=None, U_out=None, ws=None, want_u: bool = False):
+    """Y_t = X_t W'^T + s_a (X_t A_a^T) B_a^T with a = ids[t] (none if outside the
+    pool).  Returns (Y [n][dout] bf16, U [n][r] fp32 or None)."""
+    n = X.shape[0]
+    _check_multi(w, pool, X, ids, (("Y", Y, torch.bfloat16, (n, w.rows)), ("U_out", U_out, torch.float32, (n, pool.r))))
+    dev = pool.device
+    if Y is None:
+        Y = torch.empty(n, w.rows, dtype=torch.bfloat16, device=dev)
+    if U_out is None and want_u:
+        U_out = torch.empty(n, pool.r, dtype=torch.float32, device=dev)
+    ws = _multi_workspace(OP_MULTI_FWD, w, n, pool.r, ws, dev)
+    cw = w.c_struct()
+    _check("qlora_multi_fwd", lib().qlora_multi_fwd(ctypes.byref(cw), ctypes.byref(pool.c), _p(X), n, _p(ids), _p(Y),
+                                                    _p(U_out), _p(ws), ws.numel(), _stream()))
+    return Y, U_out
+
+
+def qlora_multi_bwd(w: NF4Weight, pool: AdapterPool, X, ids, dY, U=None, dX=None, dA=None, dB=None, ws=None):
+    """Returns (dX [n][din] bf16, dA [count][r][din] fp32, dB [count][dout][r] fp32)."""
+    n = X.shape[0]
+    _check_multi(w, pool, X, ids, (("dY", dY, torch.bfloat16, (n, w.rows)), ("U", U, torch.float32, (n, pool.r)),
+                                   ("dX", dX, torch.bfloat16, (n, w.cols)),
+                                   ("dA", dA, torch.float32, (pool.count, pool.r, w.cols)),
+                                   ("dB", dB, torch.float32, (pool.count, w.rows, pool.r))))
+    dev = pool.device
+    if dX is None:
+        dX = torch.empty(n, w.cols, dtype=torch.bfloat16, device=dev)
+    if dA is None:
+        dA = torch.empty(pool.count, pool.r, w.cols, dtype=torch.float32, device=dev)
+    if dB is None:
+        dB = torch.empty(pool.count, w.rows, pool.r, dtype=torch.float32, device=dev)
+    ws = _multi_workspace(OP_MULTI_BWD, w, n, pool.r, ws, dev)
+    cw = w.c_struct()
+    _check("qlora_multi_bwd", lib().qlora_multi_bwd(ctypes.byref(cw), ctypes.byref(pool.c), _p(X), n, _p(ids), _p(dY),
+                                                    _p(U), _p(dX), _p(dA), _p(dB), _p(ws), ws.numel(), _stream()))
     return dX, dA, dB
 
 

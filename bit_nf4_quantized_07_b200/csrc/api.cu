@@ -122,6 +122,59 @@ qln_status check_linear(const qln_nf4_weight *w, const uint16_t *X, int64_t n, c
 
 qln_status from_cuda(cudaError_t e) { return e == cudaSuccess ? QLN_OK : QLN_ERR_CUDA; }
 
+// Workspace of the calls with a pool of adapters (offsets 256-byte aligned):
+//   header, plan (order, start, tiles), then
+//   fwd: sU [n][r] bf16, split-K partials of U (fp32)
+//   bwd: sG, G hi, G lo, U hi, U lo [n][r] bf16, split-K partials (fp32)
+struct MultiWs {
+    size_t plan, scaled, ghi, glo, uhi, ulo, partial, total;
+};
+
+MultiWs multi_layout(bool bwd, int64_t rows, int64_t cols, int64_t n, int r) {
+    MultiWs L;
+    const size_t nr = round256((size_t)n * r * 2);
+    L.plan = qln::kWsHeaderBytes;
+    L.scaled = L.plan + qln::adapter_plan_bytes(n);
+    L.ghi = L.scaled + nr;
+    L.glo = L.ghi + (bwd ? nr : 0);
+    L.uhi = L.glo + (bwd ? nr : 0);
+    L.ulo = L.uhi + (bwd ? nr : 0);
+    L.partial = L.ulo + (bwd ? nr : 0);
+    size_t p = qln::lora_down_partial_bytes(n, cols, r, kSplitTargetSms);
+    const size_t g = bwd ? qln::lora_down_partial_bytes(n, rows, r, kSplitTargetSms) : 0;
+    L.total = L.partial + round256(p > g ? p : g);
+    return L;
+}
+
+constexpr int64_t kMaxMultiTokens = (int64_t)1 << 24;
+
+qln_status check_multi(const qln_nf4_weight *w, const qln_adapter_pool *pool, const uint16_t *X, int64_t n,
+                       const int32_t *ids) {
+    if (!pool || !ids) return QLN_ERR_NULL;
+    qln_status s = check_linear(w, X, n, pool->A, pool->B, pool->r);
+    if (s != QLN_OK) return s;
+    if (!pool->scale) return QLN_ERR_NULL;
+    if (n > kMaxMultiTokens || pool->count < 1 || pool->count > QLN_MAX_ADAPTERS) return QLN_ERR_SHAPE;
+    if (!aligned(ids, 4) || !aligned(pool->scale, 4) || !aligned(pool->rank, 4)) return QLN_ERR_ALIGN;
+    return QLN_OK;
+}
+
+// in's products down to the rank, as partials per K split; returns the splits.
+cudaError_t multi_down(const uint16_t *in, int64_t n, int64_t K, const uint16_t *factors, bool kmajor,
+                       const qln_adapter_pool *pool, const qln::AdapterPlan &plan, float *partial, int *splits,
+                       cudaStream_t st) {
+    int cps = 0;
+    qln::lora_down_plan(n, K, pool->r, kSplitTargetSms, splits, &cps);
+    return qln::launch_adapter_down(in, n, K, factors, kmajor, pool->r, pool->count, plan, partial, *splits, cps, st);
+}
+
+cudaError_t multi_gemm(const qln_nf4_weight *w, bool trans, const uint16_t *act, int64_t n, const uint16_t *lact,
+                       const uint16_t *factors, const qln_adapter_pool *pool, const int32_t *ids, uint16_t *out,
+                       cudaStream_t st) {
+    const qln::AdapterView v{ids, pool->rank, pool->count};
+    return qln::launch_nf4_mma_gemm_multi(w, trans, act, n, lact, factors, pool->r, v, out, st);
+}
+
 qln_status check_adamw_tensor(const qln_adamw_tensor &t) {
     if (!t.param || !t.grad || !t.m || !t.v) return QLN_ERR_NULL;
     if (t.n <= 0 || t.n > kMaxAdamwElems) return QLN_ERR_SHAPE;
@@ -421,6 +474,74 @@ qln_status qlora_linear_bwd(const qln_nf4_weight *w, const uint16_t *X, int64_t 
     return from_cuda(e);
 }
 
+qln_status qlora_multi_fwd(const qln_nf4_weight *w, const qln_adapter_pool *pool, const uint16_t *X, int64_t n,
+                           const int32_t *ids, uint16_t *Y, float *U_out, void *ws, size_t ws_bytes, void *stream) {
+    qln_status st = check_multi(w, pool, X, n, ids);
+    if (st != QLN_OK) return st;
+    if (!Y || !ws) return QLN_ERR_NULL;
+    if (!aligned(Y, 16) || !aligned(U_out, 16) || !aligned(ws, 256)) return QLN_ERR_ALIGN;
+    const MultiWs L = multi_layout(false, w->rows, w->cols, n, pool->r);
+    if (ws_bytes < L.total) return QLN_ERR_WORKSPACE;
+    int sms = 0;
+    st = check_device(&sms);
+    if (st != QLN_OK) return st;
+    cudaStream_t cs = (cudaStream_t)stream;
+    char *wsb = reinterpret_cast<char *>(ws);
+    const qln::AdapterPlan plan = qln::adapter_plan_at(wsb + L.plan, n);
+    uint16_t *sU = reinterpret_cast<uint16_t *>(wsb + L.scaled);
+    float *partial = reinterpret_cast<float *>(wsb + L.partial);
+    int splits = 0;
+    cudaError_t e = qln::launch_adapter_plan(ids, n, pool->count, plan, reinterpret_cast<int *>(wsb), cs);
+    if (e != cudaSuccess) return QLN_ERR_CUDA;
+    e = multi_down(X, n, w->cols, pool->A, false, pool, plan, partial, &splits, cs);
+    if (e != cudaSuccess) return QLN_ERR_CUDA;
+    e = qln::launch_adapter_fold(partial, splits, n, pool, ids, U_out, sU, nullptr, nullptr, cs);
+    if (e != cudaSuccess) return QLN_ERR_CUDA;
+    return from_cuda(multi_gemm(w, false, X, n, sU, pool->B, pool, ids, Y, cs));
+}
+
+qln_status qlora_multi_bwd(const qln_nf4_weight *w, const qln_adapter_pool *pool, const uint16_t *X, int64_t n,
+                           const int32_t *ids, const uint16_t *dY, const float *U, uint16_t *dX, float *dA, float *dB,
+                           void *ws, size_t ws_bytes, void *stream) {
+    qln_status st = check_multi(w, pool, X, n, ids);
+    if (st != QLN_OK) return st;
+    if (!dY || !dX || !dA || !dB || !ws) return QLN_ERR_NULL;
+    if (!aligned(dY, 16) || !aligned(U, 16) || !aligned(dX, 16) || !aligned(dA, 16) || !aligned(dB, 16) ||
+        !aligned(ws, 256))
+        return QLN_ERR_ALIGN;
+    const MultiWs L = multi_layout(true, w->rows, w->cols, n, pool->r);
+    if (ws_bytes < L.total) return QLN_ERR_WORKSPACE;
+    int sms = 0;
+    st = check_device(&sms);
+    if (st != QLN_OK) return st;
+    cudaStream_t cs = (cudaStream_t)stream;
+    char *wsb = reinterpret_cast<char *>(ws);
+    const qln::AdapterPlan plan = qln::adapter_plan_at(wsb + L.plan, n);
+    uint16_t *sG = reinterpret_cast<uint16_t *>(wsb + L.scaled);
+    uint16_t *Ghi = reinterpret_cast<uint16_t *>(wsb + L.ghi), *Glo = reinterpret_cast<uint16_t *>(wsb + L.glo);
+    uint16_t *Uhi = reinterpret_cast<uint16_t *>(wsb + L.uhi), *Ulo = reinterpret_cast<uint16_t *>(wsb + L.ulo);
+    float *partial = reinterpret_cast<float *>(wsb + L.partial);
+    int splits = 0;
+    cudaError_t e = qln::launch_adapter_plan(ids, n, pool->count, plan, reinterpret_cast<int *>(wsb), cs);
+    if (e != cudaSuccess) return QLN_ERR_CUDA;
+    const float *Usrc = U;  // [n][r], or the partials of its recomputation
+    int usplits = 1;
+    if (!U) {
+        e = multi_down(X, n, w->cols, pool->A, false, pool, plan, partial, &usplits, cs);
+        if (e != cudaSuccess) return QLN_ERR_CUDA;
+        Usrc = partial;
+    }
+    e = qln::launch_adapter_fold(Usrc, usplits, n, pool, ids, nullptr, nullptr, Uhi, Ulo, cs);
+    if (e != cudaSuccess) return QLN_ERR_CUDA;
+    e = multi_down(dY, n, w->rows, pool->B, true, pool, plan, partial, &splits, cs);
+    if (e != cudaSuccess) return QLN_ERR_CUDA;
+    e = qln::launch_adapter_fold(partial, splits, n, pool, ids, nullptr, sG, Ghi, Glo, cs);
+    if (e != cudaSuccess) return QLN_ERR_CUDA;
+    e = multi_gemm(w, true, dY, n, sG, pool->A, pool, ids, dX, cs);
+    if (e != cudaSuccess) return QLN_ERR_CUDA;
+    return from_cuda(qln::launch_adapter_grads(dY, Uhi, Ulo, w->rows, X, Ghi, Glo, w->cols, pool, plan, dA, dB, cs));
+}
+
 size_t qln_workspace_bytes(int32_t op, int64_t rows, int64_t cols, int64_t n, int32_t r) {
     switch (op) {
         case QLN_OP_DOUBLE_QUANT:
@@ -429,6 +550,11 @@ size_t qln_workspace_bytes(int32_t op, int64_t rows, int64_t cols, int64_t n, in
             return (rows > 0 && cols > 0 && n > 0 && r > 0) ? fwd_layout(rows, cols, n, r).total : 0;
         case QLN_OP_LINEAR_BWD:
             return (rows > 0 && cols > 0 && n > 0 && r > 0) ? bwd_layout(rows, cols, n, r).total : 0;
+        case QLN_OP_MULTI_FWD:
+        case QLN_OP_MULTI_BWD:
+            return (rows > 0 && cols > 0 && n > 0 && n <= kMaxMultiTokens && r > 0)
+                       ? multi_layout(op == QLN_OP_MULTI_BWD, rows, cols, n, r).total
+                       : 0;
         case QLN_OP_QUANTIZE_DQ_BATCH:
             return (rows > 0 && rows <= kMaxBatchJobs) ? qln::kDqBatchScratchBytes * (size_t)rows : 0;
         default:
@@ -458,7 +584,7 @@ const char *qln_status_str(qln_status st) {
     }
 }
 
-int32_t qln_version(void) { return (1 << 16) | 0; }
+int32_t qln_version(void) { return (1 << 16) | 1; }
 
 uint64_t qln_launch_count(void) { return qln::g_launches.load(std::memory_order_relaxed); }
 

@@ -15,6 +15,11 @@
 //                            (act = dY, lact = s*G, lw = A, out = dX)
 // A 64x64 tile of W' is decoded per k-step into shared memory (W' never
 // reaches HBM); ldmatrix (.trans for dX) feeds the MMA.
+//
+// MULTI: each token has an adapter of its own from a pool (lw is the pool's
+// base).  The adapters present among the tile's tokens are taken in turn, and
+// a product is added to its own tokens' sums only, so that no value of one
+// adapter reaches another's tokens.
 #include "qln_common.cuh"
 #include "qln_internal.h"
 
@@ -29,7 +34,7 @@ struct SmemSm80 {
     float cb[16];
 };
 
-template <bool TRANS>
+template <bool TRANS, bool MULTI>
 __global__ void __launch_bounds__(128) nf4_mma_gemm_kernel(const uint8_t *__restrict__ codes,
                                                            const float *__restrict__ absmax,
                                                            const int8_t *__restrict__ qabs,
@@ -38,7 +43,7 @@ __global__ void __launch_bounds__(128) nf4_mma_gemm_kernel(const uint8_t *__rest
                                                            int64_t cols, const uint16_t *__restrict__ act, int64_t n,
                                                            const uint16_t *__restrict__ lact,
                                                            const uint16_t *__restrict__ lw, int r,
-                                                           uint16_t *__restrict__ out, bool e4m3) {
+                                                           uint16_t *__restrict__ out, bool e4m3, const AdapterView av) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     pdl_wait();  // every input may come from the previous kernel on the stream
     pdl_trigger();
@@ -98,7 +103,8 @@ __global__ void __launch_bounds__(128) nf4_mma_gemm_kernel(const uint8_t *__rest
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
 
-    auto mma_tile = [&](const uint16_t *Abase, int a_ld, bool a_trans, const uint16_t *Bbase, int b_ld, int kk) {
+    auto mma_tile = [&](float (&acc)[2][4][4], const uint16_t *Abase, int a_ld, bool a_trans, const uint16_t *Bbase,
+                        int b_ld, int kk) {
         uint32_t a[2][4], b[4][2];
         const int mat = lane >> 3;
 #pragma unroll
@@ -161,13 +167,68 @@ __global__ void __launch_bounds__(128) nf4_mma_gemm_kernel(const uint8_t *__rest
         }
         __syncthreads();
 #pragma unroll
-        for (int kk = 0; kk < kSmBK; kk += 16) mma_tile(&S.w[0][0], kSmPad, TRANS, &S.act[buf][0][0], kSmPad, kk);
+        for (int kk = 0; kk < kSmBK; kk += 16) mma_tile(acc, &S.w[0][0], kSmPad, TRANS, &S.act[buf][0][0], kSmPad, kk);
         __syncthreads();
         ah = ah_next;
     }
 
     // Adapter term as extra K steps over j (zero-padded to a multiple of 16).
-    {
+    if constexpr (MULTI) {
+        __shared__ int s_id[64], s_first[64];
+        if (tid < 64) {
+            const int a = t0 + tid < n ? __ldg(av.ids + t0 + tid) : -1;
+            s_id[tid] = (unsigned)a < (unsigned)av.count ? a : -1;
+        }
+        __syncthreads();
+        if (tid < 64) {
+            bool first = s_id[tid] >= 0;
+            for (int u = 0; u < tid && first; ++u) first = s_id[u] != s_id[tid];
+            s_first[tid] = first;
+        }
+        __syncthreads();
+        const int cpr = rpad / 8, rc = r / 8;
+        for (int u = 0; u < 64; ++u) {
+            if (!s_first[u]) continue;
+            const int a = s_id[u];
+            const int k0 = av.rank ? __ldg(av.rank + a) : r, rk = k0 < 0 ? 0 : (k0 > r ? r : k0);
+            const uint16_t *lwa = lw + (int64_t)a * r * M;
+            const int ls_chunks = TRANS ? rpad * 8 : 64 * cpr;
+            for (int idx = tid; idx < ls_chunks; idx += 128) {
+                const int row = TRANS ? idx >> 3 : idx / cpr, ck = TRANS ? idx & 7 : idx % cpr;
+                const bool ok = TRANS ? row < rk : ck < rc;
+                const uint16_t *src = TRANS ? lwa + (int64_t)row * cols + m0 + 8 * ck : lwa + (m0 + row) * r + 8 * ck;
+                cp_async16_zfill(Ls + row * ls_ld + 8 * ck, ok ? src : lw, ok ? 16 : 0);
+            }
+            for (int idx = tid; idx < 64 * cpr; idx += 128) {
+                const int row = idx / cpr, ck = idx % cpr;
+                const bool ok = s_id[row] == a && ck < rc;
+                cp_async16_zfill(Ms + row * ms_ld + 8 * ck, ok ? lact + (t0 + row) * r + 8 * ck : lact, ok ? 16 : 0);
+            }
+            cp_async_commit();
+            cp_async_wait<0>();
+            __syncthreads();
+            if (!TRANS && rk < r) {  // columns past the rank take no part, whatever they hold
+                for (int idx = tid; idx < 64 * (r - rk); idx += 128) Ls[(idx / (r - rk)) * ls_ld + rk + idx % (r - rk)] = 0;
+                __syncthreads();
+            }
+            float own[2][4][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) own[i][j][e] = 0.f;
+            for (int kk = 0; kk < rk; kk += 16) mma_tile(own, Ls, ls_ld, TRANS, Ms, ms_ld, kk);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (s_id[wn * 32 + j * 8 + 2 * c + (e & 1)] == a) acc[i][j][e] = __fadd_rn(acc[i][j][e], own[i][j][e]);
+            __syncthreads();
+        }
+    } else {
         const int cpr = rpad / 8;  // 16-byte chunks per adapter row (padded)
         const int rc = r / 8;      // real chunks (r % 8 == 0)
         // Ls: fwd rows m (lw = B [rows][r]); dX rows j (lw = A [r][cols])
@@ -198,7 +259,7 @@ __global__ void __launch_bounds__(128) nf4_mma_gemm_kernel(const uint8_t *__rest
         cp_async_commit();
         cp_async_wait<0>();
         __syncthreads();
-        for (int kk = 0; kk < rpad; kk += 16) mma_tile(Ls, ls_ld, TRANS, Ms, ms_ld, kk);
+        for (int kk = 0; kk < rpad; kk += 16) mma_tile(acc, Ls, ls_ld, TRANS, Ms, ms_ld, kk);
         __syncthreads();
     }
 
@@ -225,11 +286,10 @@ __global__ void __launch_bounds__(128) nf4_mma_gemm_kernel(const uint8_t *__rest
     }
 }
 
-cudaError_t launch_nf4_mma_gemm(const qln_nf4_weight *w, bool trans, const uint16_t *act, int64_t n,
-                                const uint16_t *lact, const uint16_t *lw, int r, uint16_t *out, int *status,
-                                cudaStream_t st, int num_sms) {
-    (void)status;
-    (void)num_sms;
+template <bool MULTI>
+static cudaError_t launch_mma_t(const qln_nf4_weight *w, bool trans, const uint16_t *act, int64_t n,
+                                const uint16_t *lact, const uint16_t *lw, int r, const AdapterView &v, uint16_t *out,
+                                cudaStream_t st) {
     const int rpad = (r + 15) & ~15;
     const int ls_ld = trans ? kSmPad : rpad + 8;
     const int ls_rows = trans ? rpad : 64;
@@ -237,11 +297,25 @@ cudaError_t launch_nf4_mma_gemm(const qln_nf4_weight *w, bool trans, const uint1
     const int64_t M = trans ? w->cols : w->rows;
     dim3 grid((unsigned)((n + kSmBN - 1) / kSmBN), (unsigned)(M / kSmBM));
     const bool e4m3 = w->dq_format == QLN_DQ_E4M3;
-    auto kern = trans ? nf4_mma_gemm_kernel<true> : nf4_mma_gemm_kernel<false>;
+    auto kern = trans ? nf4_mma_gemm_kernel<true, MULTI> : nf4_mma_gemm_kernel<false, MULTI>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, grid, dim3(128), smem, st, w->codes, w->absmax, w->qabs, w->dq_scale, w->dq_mean, w->rows,
-                      w->cols, act, n, lact, lw, r, out, e4m3);
+                      w->cols, act, n, lact, lw, r, out, e4m3, v);
+}
+
+cudaError_t launch_nf4_mma_gemm(const qln_nf4_weight *w, bool trans, const uint16_t *act, int64_t n,
+                                const uint16_t *lact, const uint16_t *lw, int r, uint16_t *out, int *status,
+                                cudaStream_t st, int num_sms) {
+    (void)status;
+    (void)num_sms;
+    return launch_mma_t<false>(w, trans, act, n, lact, lw, r, AdapterView{}, out, st);
+}
+
+cudaError_t launch_nf4_mma_gemm_multi(const qln_nf4_weight *w, bool trans, const uint16_t *act, int64_t n,
+                                      const uint16_t *lact, const uint16_t *lw, int r, const AdapterView &v,
+                                      uint16_t *out, cudaStream_t st) {
+    return launch_mma_t<true>(w, trans, act, n, lact, lw, r, v, out, st);
 }
 
 }  // namespace qln

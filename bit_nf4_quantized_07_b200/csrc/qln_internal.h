@@ -101,12 +101,42 @@ cudaError_t launch_tn_skinny_side(const uint16_t *dY, const uint16_t *U, int64_t
 int64_t nf4_tc_gemm_ctas(const qln_nf4_weight *w, bool trans, int64_t n, int r, int num_sms);
 int tn_skinny_splits(int64_t n, int64_t M, int R, int num_sms);
 
+// adapters.cu: a pool of adapters, one per token (ids outside 0 .. count - 1: none).
+struct AdapterPlan {  // device arrays of the grouping by adapter (see adapter_plan_kernel)
+    int32_t *order, *start, *tiles;
+};
+size_t adapter_plan_bytes(int64_t n);
+AdapterPlan adapter_plan_at(void *base, int64_t n);  // 256-byte aligned base of adapter_plan_bytes(n)
+cudaError_t launch_adapter_plan(const int32_t *ids, int64_t n, int count, const AdapterPlan &p, int *status, cudaStream_t st);
+// partial[split][t][j] = in[t] . factor_a(t)[j] over one of the K ranges of cps 64-chunks
+cudaError_t launch_adapter_down(const uint16_t *in, int64_t n, int64_t K, const uint16_t *pool, bool kmajor, int r,
+                                int count, const AdapterPlan &p, float *partial, int splits, int cps, cudaStream_t st);
+// the splits' sum as fp32, as bf16(s v) and as a bf16 pair (each may be null)
+cudaError_t launch_adapter_fold(const float *partial, int splits, int64_t n, const qln_adapter_pool *pool,
+                                const int32_t *ids, float *full, uint16_t *scaled, uint16_t *hi, uint16_t *lo, cudaStream_t st);
+cudaError_t launch_adapter_grads(const uint16_t *dY, const uint16_t *Uhi, const uint16_t *Ulo, int64_t dout,
+                                 const uint16_t *X, const uint16_t *Ghi, const uint16_t *Glo, int64_t din,
+                                 const qln_adapter_pool *pool, const AdapterPlan &p, float *dA, float *dB, cudaStream_t st);
+// split-K plan of the down products (lora_small.cu)
+void lora_down_plan(int64_t n, int64_t K, int r, int num_sms, int *splits, int *cps);
+
+// The adapters of a GEMM over tokens with adapters of their own: lact is
+// bf16(s U) [n][r] and lw the pool's factor base, `stride` elements per adapter.
+struct AdapterView {
+    const int32_t *ids, *rank;
+    int count;
+};
+
 // nf4_gemm_sm80.cu: fused NF4 decode + legacy mma.sync GEMM (small n).
 //   trans = false: out[t][m] = bf16(sum_k act[t][k] W'[m][k] + sum_j lact[t][j] lw[m][j])   (forward)
 //   trans = true : out[t][m] = bf16(sum_k act[t][k] W'[k][m] + sum_j lact[t][j] lw[j][m])   (dX)
 cudaError_t launch_nf4_mma_gemm(const qln_nf4_weight *w, bool trans, const uint16_t *act, int64_t n,
                                 const uint16_t *lact, const uint16_t *lw, int r, uint16_t *out,
                                 int *status, cudaStream_t st, int num_sms);
+// the same with lw the factors of a pool, one adapter per token
+cudaError_t launch_nf4_mma_gemm_multi(const qln_nf4_weight *w, bool trans, const uint16_t *act, int64_t n,
+                                      const uint16_t *lact, const uint16_t *lw, int r, const AdapterView &v,
+                                      uint16_t *out, cudaStream_t st);
 
 // 2D tiled TMA descriptor over a row-major [outer][inner] array (nf4_gemm_sm100.cu).
 bool make_tensor_map_2d(CUtensorMap *m, CUtensorMapDataType dt, int esize, const void *base, uint64_t inner,

@@ -93,7 +93,8 @@ enum { QLN_DQ_INT8 = 0, QLN_DQ_E4M3 = 1 };
 enum { QLN_DTYPE_F32 = 0, QLN_DTYPE_BF16 = 1, QLN_DTYPE_F16 = 2 };
 
 /* Workspace-sized operations (qln_workspace_bytes `op`). */
-enum { QLN_OP_DOUBLE_QUANT = 1, QLN_OP_LINEAR_FWD = 2, QLN_OP_LINEAR_BWD = 3, QLN_OP_QUANTIZE_DQ_BATCH = 4 };
+enum { QLN_OP_DOUBLE_QUANT = 1, QLN_OP_LINEAR_FWD = 2, QLN_OP_LINEAR_BWD = 3, QLN_OP_QUANTIZE_DQ_BATCH = 4,
+       QLN_OP_MULTI_FWD = 5, QLN_OP_MULTI_BWD = 6 };
 
 /* An NF4 weight as stored by nf4_quantize (+ nf4_double_quant).  All pointers
  * are device pointers owned by the caller.  With qabs != NULL the weight is
@@ -359,6 +360,66 @@ QLN_API qln_status qlora_linear_bwd(const qln_nf4_weight *w, const uint16_t *X, 
                             const uint16_t *A, const uint16_t *B, int32_t r, float s,
                             const uint16_t *dY, const uint16_t *U, uint16_t *dX, float *dA,
                             float *dB, void *ws, size_t ws_bytes, void *stream);
+
+/* Adapters of one pool, at most. */
+enum { QLN_MAX_ADAPTERS = 1024 };
+
+/* A pool of LoRA adapters beside one NF4 weight.  All pointers are device
+ * pointers owned by the caller; the tables may change between calls, and
+ * between the replays of a captured call. */
+typedef struct {
+    const uint16_t *A;   /* [count][r][din] bf16                              */
+    const uint16_t *B;   /* [count][dout][r] bf16                             */
+    const float *scale;  /* [count] s of each adapter                         */
+    const int32_t *rank; /* [count] rank of each adapter, or NULL: all r.  Rows
+                          * of A and columns of B past it take no part,
+                          * whatever they hold.  Values outside 0 .. r are
+                          * taken as the nearer end.                          */
+    int32_t count;       /* 1 .. QLN_MAX_ADAPTERS                             */
+    int32_t r;           /* a multiple of 8 in 8 .. 128                       */
+} qln_adapter_pool;
+
+/*
+ * qlora_multi_fwd -- qlora_linear_fwd of a batch whose tokens belong to
+ * different adapters: the requests of a server, or several adapters in
+ * training, over one shared NF4 weight.
+ * Defined by the passages that qlora_linear_fwd cites; token t has the adapter
+ * a = ids[t], and none (only X W'^T) if a is outside 0 .. count - 1.
+ *   X [n][din] bf16 in; ids [n] int32 in (device), in any order;
+ *   Y [n][dout] bf16 out = bf16_RN(X_t W'^T + s_a (X_t A_a^T) B_a^T), fp32
+ *   accumulation, with bf16(s_a U_t) as the tensor cores' operand;
+ *   U_out [n][r] fp32 out (nullable): U_t = X_t A_a^T, unscaled, zero past the
+ *   adapter's rank and for tokens without one, for reuse by qlora_multi_bwd.
+ * A token's row of Y and U depends on its own row of X and its own adapter
+ * only: infinities and NaN of other adapters and tokens do not reach it.
+ *   ws: at least qln_workspace_bytes(QLN_OP_MULTI_FWD, dout, din, n, r) bytes,
+ *   256-byte aligned; byte 0 holds the device status word afterwards.  Calls
+ *   that may run at the same time need workspaces of their own.
+ * Errors: QLN_ERR_NULL; QLN_ERR_SHAPE (n < 1 or above 2^24; count; r; rows or
+ * cols not a multiple of 64); QLN_ERR_ALIGN (16-byte: codes, X, A, B, Y, U_out;
+ * 4-byte: ids, scale, rank; ws 256-byte); QLN_ERR_WORKSPACE; QLN_ERR_ARCH.
+ */
+QLN_API qln_status qlora_multi_fwd(const qln_nf4_weight *w, const qln_adapter_pool *pool, const uint16_t *X, int64_t n,
+                                   const int32_t *ids, uint16_t *Y, float *U_out, void *ws, size_t ws_bytes,
+                                   void *stream);
+
+/*
+ * qlora_multi_bwd -- the backward pass of qlora_multi_fwd.
+ * Defined by the passages that qlora_linear_bwd cites.  For upstream dY, with
+ * G_t = dY_t B_a:
+ *   dX_t = dY_t W' + s_a G_t A_a               [n][din]         bf16 out
+ *   dA_a = s_a sum over a's tokens G_t^T X_t   [count][r][din]  fp32 out
+ *   dB_a = s_a sum over a's tokens dY_t^T U_t  [count][dout][r] fp32 out
+ * Every element of dA and dB is written: zero for adapters without tokens and
+ * past an adapter's rank.  Sums run in an order fixed by the sizes and ids.
+ * U (nullable) is U_out of the matching forward; when NULL it is recomputed.
+ * G and U enter dA and dB with 16 bits of mantissa and fp32 accumulation.
+ * ws: at least qln_workspace_bytes(QLN_OP_MULTI_BWD, dout, din, n, r) bytes.
+ * Errors: as qlora_multi_fwd, for dY, dX, dA and dB too.
+ */
+QLN_API qln_status qlora_multi_bwd(const qln_nf4_weight *w, const qln_adapter_pool *pool, const uint16_t *X, int64_t n,
+                                   const int32_t *ids, const uint16_t *dY, const float *U, uint16_t *dX, float *dA,
+                                   float *dB, void *ws, size_t ws_bytes, void *stream);
 
 /* AdamW hyper-parameters (fp32, as the update computes in fp32). */
 typedef struct {
