@@ -170,8 +170,10 @@ cudaError_t multi_down(const uint16_t *in, int64_t n, int64_t K, const uint16_t 
 
 cudaError_t multi_gemm(const qln_nf4_weight *w, bool trans, const uint16_t *act, int64_t n, const uint16_t *lact,
                        const uint16_t *factors, const qln_adapter_pool *pool, const int32_t *ids, uint16_t *out,
-                       cudaStream_t st) {
+                       int *status, cudaStream_t st, int num_sms) {
     const qln::AdapterView v{ids, pool->rank, pool->count};
+    if (qln::nf4_tc_gemm_supported(w, trans, n, pool->r))
+        return qln::launch_nf4_tc_gemm_multi(w, trans, act, n, lact, factors, pool->r, v, out, status, st, num_sms);
     return qln::launch_nf4_mma_gemm_multi(w, trans, act, n, lact, factors, pool->r, v, out, st);
 }
 
@@ -497,7 +499,7 @@ qln_status qlora_multi_fwd(const qln_nf4_weight *w, const qln_adapter_pool *pool
     if (e != cudaSuccess) return QLN_ERR_CUDA;
     e = qln::launch_adapter_fold(partial, splits, n, pool, ids, U_out, sU, nullptr, nullptr, cs);
     if (e != cudaSuccess) return QLN_ERR_CUDA;
-    return from_cuda(multi_gemm(w, false, X, n, sU, pool->B, pool, ids, Y, cs));
+    return from_cuda(multi_gemm(w, false, X, n, sU, pool->B, pool, ids, Y, reinterpret_cast<int *>(wsb), cs, sms));
 }
 
 qln_status qlora_multi_bwd(const qln_nf4_weight *w, const qln_adapter_pool *pool, const uint16_t *X, int64_t n,
@@ -537,7 +539,7 @@ qln_status qlora_multi_bwd(const qln_nf4_weight *w, const qln_adapter_pool *pool
     if (e != cudaSuccess) return QLN_ERR_CUDA;
     e = qln::launch_adapter_fold(partial, splits, n, pool, ids, nullptr, sG, Ghi, Glo, cs);
     if (e != cudaSuccess) return QLN_ERR_CUDA;
-    e = multi_gemm(w, true, dY, n, sG, pool->A, pool, ids, dX, cs);
+    e = multi_gemm(w, true, dY, n, sG, pool->A, pool, ids, dX, reinterpret_cast<int *>(wsb), cs, sms);
     if (e != cudaSuccess) return QLN_ERR_CUDA;
     return from_cuda(qln::launch_adapter_grads(dY, Uhi, Ulo, w->rows, X, Ghi, Glo, w->cols, pool, plan, dA, dB, cs));
 }

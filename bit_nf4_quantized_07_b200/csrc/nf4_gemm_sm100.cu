@@ -24,6 +24,18 @@
 //   B_op (activations X / dY, K-major): TMA tiles with 128-byte swizzle;
 //   the adapter term is extra K steps whose A_op (B or A, zero-padded to 64)
 //     and B_op (s*U or s*G) both arrive by TMA.
+// MULTI: each token has an adapter of its own from a pool.  The adapter term
+// takes ceil(rank / 64) k-steps per adapter present among the tile's tokens, in
+// the order of their first tokens (warp 1 lists them while the pipeline
+// fills).  Such a step's A_op is the adapter's factor by TMA (3-D map, so rows
+// past the factor read as zero); its B_op is written by the decoders, s*U or
+// s*G of the adapter's own tokens and zero for the others (all MMAs keep one
+// shape: only then do they run in the order of their issue).  A zero times an
+// infinity would still be a NaN, so the decoders also replace what is not
+// finite in the factor's tile by zero, and the epilogue adds those products
+// to their own tokens one by one (a path that finite factors never take).
+// An adapter step costs as much as a weight step at most; a prefill tile of
+// packed sequences has one or two.
 // Warp roles: warp 0 TMA producer, warp 1 TMEM owner + single-thread MMA
 // issuer, warps 2.. decoders and then the epilogue (TMEM -> BF16 -> HBM).
 // Every barrier wait is bounded; on give-up the CTA records QLN_ERR_TIMEOUT
@@ -56,11 +68,39 @@ struct Cfg {
     static constexpr uint32_t kOffB = kOffA + kStages * kABytes;
     static constexpr uint32_t kOffC = kOffB + kStages * kBBytes;
     static constexpr uint32_t kOffBar = kOffC + kStages * kCBytes;
-    // barriers: tma_full[S], code_full[S], dec_full[S], empty[S], accum_full
-    static constexpr uint32_t kNumBars = 4 * kStages + 1;
+    // barriers: tma_full[S], code_full[S], dec_full[S], empty[S], accum_full, list_full (MULTI)
+    static constexpr uint32_t kNumBars = 4 * kStages + 2;
     static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;  // tmem base, abort flag, epilogue go
     static constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;  // + alignment slack
+    // MULTI: the tile's adapters (16-bit entries: the adapter of each token, then the list: adapter, first and last
+    // token; and the list's place of every adapter of the pool)
+    static constexpr int kTok = NT * kMaxBN;
+    static constexpr uint32_t kOffList = kOffMisc + 16;
+    static constexpr uint32_t kListBytes = (4 * kTok + QLN_MAX_ADAPTERS) * 2 + 16;
+    static constexpr uint32_t kSmemBytesMulti = kSmemBytes + kListBytes;
+    static_assert(kSmemBytesMulti <= 232448, "shared memory of one CTA");
 };
+
+// The pool's side of a MULTI call.
+struct MultiParams {
+    const int32_t *ids, *rank;
+    const uint16_t *lact;  // [n][r] bf16: s U or s G
+    const uint16_t *lw;    // the pool's factors
+    int count, r;
+};
+
+// What the products of a factor's non-finite elements add to one output (m, t)
+// of adapter a: lw rows of m with stride 1 over j (forward) or columns with
+// stride M (dX).
+__device__ __noinline__ float nonfinite_products(const MultiParams &mp, int a, int64_t m, int64_t t, int64_t M, bool trans) {
+    float v = 0.f;
+    const int rk = mp.rank ? min(max(__ldg(mp.rank + a), 0), mp.r) : mp.r;
+    for (int j = 0; j < rk; ++j) {
+        const uint32_t f = mp.lw[trans ? ((int64_t)a * mp.r + j) * M + m : ((int64_t)a * M + m) * mp.r + j];
+        if ((f & 0x7f80u) == 0x7f80u) v += bf16lo_to_f32(f) * bf16lo_to_f32(mp.lact[t * mp.r + j]);
+    }
+    return v;
+}
 
 struct Params {
     const int8_t *qabs;
@@ -78,11 +118,11 @@ struct Params {
     int BN;            // tokens per accumulator (multiple of 16)
 };
 
-template <bool TRANS, int MT, int NT>
+template <bool TRANS, int MT, int NT, bool MULTI>
 __global__ void __launch_bounds__(Cfg<MT, NT>::kThreads, 1)
 nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_act,
                    const __grid_constant__ CUtensorMap tm_lw, const __grid_constant__ CUtensorMap tm_lact,
-                   const Params p) {
+                   const Params p, const MultiParams mp) {
     using C = Cfg<MT, NT>;
     constexpr int S = C::kStages;
     constexpr int TM = kBM * MT;  // rows of the CTA tile
@@ -95,6 +135,7 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
     auto dec_full = [&](int s) { return bar0 + 8u * (2 * S + s); };
     auto empty = [&](int s) { return bar0 + 8u * (3 * S + s); };
     const uint32_t accum_full = bar0 + 8u * (4 * S);
+    const uint32_t list_full = bar0 + 8u * (4 * S + 1);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 4);
     volatile int *epi_go = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 8);
@@ -102,7 +143,21 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t0 = (int64_t)blockIdx.x * NT * p.BN;  // NT accumulators of BN tokens each
     const int64_t m0 = (int64_t)blockIdx.y * TM;
-    const int nsteps = p.KT + p.RT;
+    const int nsteps = p.KT + (MULTI ? 0 : p.RT);
+    // MULTI: the tile's adapters
+    int16_t *s_tok = reinterpret_cast<int16_t *>(smem + C::kOffList);
+    int16_t *s_who = s_tok + C::kTok, *s_first = s_who + C::kTok, *s_last = s_first + C::kTok, *s_place = s_last + C::kTok;
+    volatile int *s_count = reinterpret_cast<volatile int *>(s_place + QLN_MAX_ADAPTERS);  // adapters of the tile
+    volatile int *s_bad = s_count + 1;                                                     // a factor is not finite
+    auto rank_of = [&](int a) -> int {
+        if (!mp.rank) return mp.r;
+        const int k = __ldg(mp.rank + a);
+        return k < 0 ? 0 : (k > mp.r ? mp.r : k);
+    };
+    // whether the list's adapter e may have tokens in sub-tile nt (first and last token of the tile)
+    auto in_sub = [&](int e, int nt) -> bool { return s_first[e] < (nt + 1) * p.BN && s_last[e] >= nt * p.BN; };
+    if (MULTI)
+        for (int i = threadIdx.x; i < QLN_MAX_ADAPTERS; i += C::kThreads) s_place[i] = -1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -113,11 +168,15 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
         }
         mbar_init(accum_full, 1);
         *abort_flag = 0;
+        if (MULTI) {
+            mbar_init(list_full, 1);
+            *s_bad = 0;
+        }
         mbar_fence_init();
         tma_prefetch_map(&tm_codes);
         tma_prefetch_map(&tm_act);
         tma_prefetch_map(&tm_lw);
-        tma_prefetch_map(&tm_lact);
+        if (!MULTI) tma_prefetch_map(&tm_lact);
     }
     if (warp == 1) {
         tmem_alloc(smem_addr(tmem_slot), C::kTmemCols);
@@ -182,6 +241,33 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                 }
                 issued = kt + 1;
             }
+            if constexpr (MULTI) {
+                if (issued == nsteps && !mbar_wait_bounded(list_full, 0, abort_flag, kWaitLimitNs)) {
+                    give_up();
+                } else if (issued == nsteps) {
+                    const int na = *s_count;
+                    for (int e = 0; e < na && !*abort_flag; ++e) {
+                        const int a = s_who[e], rk = rank_of(a);
+                        for (int j = 0; j < rk; j += kBK) {
+                            const int s = issued % S;
+                            if (!mbar_wait_bounded(empty(s), ((uint32_t)(issued / S) & 1u) ^ 1u, abort_flag, kWaitLimitNs)) {
+                                give_up();
+                                break;
+                            }
+                            const uint32_t sA = sbase + C::kOffA + s * C::kABytes;
+                            mbar_arrive_expect_tx(tma_full(s), C::kABytes);
+                            if (!TRANS) {
+                                tma_load_3d(sA, &tm_lw, j, (int32_t)m0, a, tma_full(s));
+                            } else {
+#pragma unroll
+                                for (int d = 0; d < 2 * MT; ++d)
+                                    tma_load_3d(sA + 8192 * d, &tm_lw, (int32_t)m0 + 64 * d, j, a, tma_full(s));
+                            }
+                            ++issued;
+                        }
+                    }
+                }
+            }
             // Drain: every issued copy has landed before the CTA may exit.
             for (int kt = (issued > S ? issued - S : 0); kt < issued; ++kt) {
                 const int s = kt % S;
@@ -192,6 +278,42 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
+        if constexpr (MULTI) {
+            // the tile's adapters, in the order of their first tokens
+            int id[(C::kTok + 31) / 32];
+            const int ntok = NT * p.BN;
+#pragma unroll
+            for (int i = 0; i < (C::kTok + 31) / 32; ++i) {
+                const int k = 32 * i + lane;
+                const int a = k < ntok && t0 + k < p.n ? __ldg(mp.ids + t0 + k) : -1;
+                id[i] = (unsigned)a < (unsigned)mp.count ? a : -1;
+                if (k < ntok) s_tok[k] = (int16_t)id[i];
+            }
+            int na = 0;
+#pragma unroll
+            for (int i = 0; i < (C::kTok + 31) / 32; ++i) {
+                const uint32_t same = __match_any_sync(0xffffffffu, id[i]);
+                const bool lead = id[i] >= 0 && (same & ((1u << lane) - 1u)) == 0;
+                int at = lead ? s_place[id[i]] : 0;
+                const uint32_t fresh = __ballot_sync(0xffffffffu, lead && at < 0);
+                if (lead) {
+                    if (at < 0) {
+                        at = na + __popc(fresh & ((1u << lane) - 1u));
+                        s_place[id[i]] = (int16_t)at;
+                        s_who[at] = (int16_t)id[i];
+                        s_first[at] = (int16_t)(32 * i + lane);
+                    }
+                    s_last[at] = (int16_t)(32 * i + 31 - __clz(same));
+                }
+                na += __popc(fresh);
+                __syncwarp();
+            }
+            if (lane == 0) {
+                *s_count = na;
+                mbar_arrive(list_full);  // release: the list above is visible to its waiters
+            }
+            __syncwarp();
+        }
         if (lane == 0) {
             const uint32_t idesc = idesc_bf16_f32(kBM, p.BN, TRANS, false);
             for (int kt = 0; kt < nsteps; ++kt) {
@@ -222,6 +344,39 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                     }
                 }
                 tc_commit(empty(s));
+            }
+            if constexpr (MULTI) {
+                const int na = *s_count;
+                int kt = nsteps;
+                for (int e = 0; e < na && !*abort_flag; ++e) {
+                    const int rk = rank_of(s_who[e]);
+                    for (int j = 0; j < rk; j += kBK, ++kt) {
+                        const int s = kt % S;
+                        const uint32_t ph = (uint32_t)(kt / S) & 1u;
+                        if (!mbar_wait_bounded(tma_full(s), ph, abort_flag, kWaitLimitNs) ||
+                            !mbar_wait_bounded(dec_full(s), ph, abort_flag, kWaitLimitNs)) {
+                            give_up();
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t sA = sbase + C::kOffA + s * C::kABytes;
+                        const uint32_t sB = sbase + C::kOffB + s * C::kBBytes;
+                        const int ks = rk - j < kBK ? (rk - j + 15) / 16 : kBK / 16;
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if (!in_sub(e, nt)) continue;
+                            for (int sub = 0; sub < MT; ++sub) {
+                                const uint32_t aS = sA + sub * 16384;
+                                for (int k = 0; k < ks; ++k) {
+                                    const uint64_t adesc = TRANS ? smem_desc_sw128(aS + k * 2048, 8192, 1024)
+                                                                 : smem_desc_sw128(aS + k * 32, 16, 1024);
+                                    const uint64_t bdesc = smem_desc_sw128(sB + nt * p.BN * 128 + k * 32, 16, 1024);
+                                    tc_mma_ss(tmem_d + (sub * NT + nt) * 256, adesc, bdesc, idesc, 1u);
+                                }
+                            }
+                        }
+                        tc_commit(empty(s));
+                    }
+                }
             }
             tc_commit(accum_full);
         }
@@ -305,6 +460,68 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
             }
             mbar_arrive(dec_full(s));
         }
+        if constexpr (MULTI) {
+            if (!*abort_flag && !mbar_wait_bounded(list_full, 0, abort_flag, kWaitLimitNs)) give_up();
+            const int na = *abort_flag ? 0 : *s_count;
+            int kt = nsteps;
+            for (int e = 0; e < na && !*abort_flag; ++e) {
+                const int a = s_who[e], rk = rank_of(a);
+                for (int j = 0; j < rk; j += kBK, ++kt) {
+                    const int s = kt % S;
+                    const uint32_t ph = (uint32_t)(kt / S) & 1u;
+                    if (!mbar_wait_bounded(empty(s), ph ^ 1u, abort_flag, kWaitLimitNs)) {
+                        give_up();
+                        break;
+                    }
+                    const int left = rk - j < kBK ? rk - j : kBK, cks = 2 * ((left + 15) / 16);  // 8-wide chunks
+                    const uint32_t sB = sbase + C::kOffB + s * C::kBBytes;
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const int work = in_sub(e, nt) ? p.BN * cks : 0;
+#pragma unroll 4
+                        for (int i = dt; i < work; i += C::kDecThreads) {
+                            const int row = i / cks, c = i % cks, k = nt * p.BN + row;
+                            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                            if (s_tok[k] == a && j + 8 * c < mp.r)
+                                v = __ldcg(reinterpret_cast<const uint4 *>(mp.lact + (t0 + k) * mp.r + j + 8 * c));
+                            st_shared_v4(sB + (nt * p.BN + row) * 128 + ((c ^ (row & 7)) << 4), v);
+                        }
+                    }
+                    if (!mbar_wait_bounded(tma_full(s), ph, abort_flag, kWaitLimitNs)) {
+                        give_up();
+                        break;
+                    }
+                    // The factor's tile: zero past the rank, and where it is not finite.  One thread per
+                    // 128-byte row: 64 columns j of one m, or 64 m of one row j.
+                    uint8_t *row = smem + C::kOffA + s * C::kABytes + (TRANS ? dcol * 8192 + drow * 128 : dt * 128);
+                    const int r7 = (TRANS ? drow : dt) & 7;
+                    const bool past = TRANS && drow >= left;  // the whole row is past the rank
+                    bool bad = false;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        if (TRANS ? drow >= 8 * cks : c >= cks) continue;  // the MMA does not read it
+                        uint4 *q = reinterpret_cast<uint4 *>(row + ((c ^ r7) << 4));
+                        const uint4 v = *q;
+                        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                        bool fix = false;
+#pragma unroll
+                        for (int h = 0; h < 8; ++h) {
+                            const uint32_t x = (w[h >> 1] >> (16 * (h & 1))) & 0xffffu;
+                            const bool out = TRANS ? past : 8 * c + h >= left;
+                            const bool inf = (x & 0x7f80u) == 0x7f80u && !out;
+                            bad |= inf;
+                            if ((inf || out) && x) {
+                                w[h >> 1] &= (h & 1) ? 0x0000ffffu : 0xffff0000u;
+                                fix = true;
+                            }
+                        }
+                        if (fix) *q = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    if (bad) *s_bad = 1;
+                    fence_proxy_async_smem();
+                    mbar_arrive(dec_full(s));
+                }
+            }
+        }
 
         // ------------------------------------------------------------ epilogue
         // The go / no-go decision is made uniform across the decoder threads
@@ -319,6 +536,9 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
             const int sub = (warp - 2) >> 2;     // weight sub-tile of this warp
             uint16_t *Os = reinterpret_cast<uint16_t *>(smem);  // [NT*BN][TM] bf16; all MMAs are done
             const int m = sub * kBM + q * 32 + lane;
+            const bool bad = MULTI && *s_bad;
+            // (the output tile overwrites the stages, not the list behind them)
+            auto tok_id = [&](int k) -> int { return s_tok[k]; };
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 for (int c0 = 0; c0 < p.BN; c0 += 32) {
@@ -327,9 +547,16 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                     tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        if (c0 + j < p.BN)
-                            Os[(nt * p.BN + c0 + j) * TM + m] =
-                                __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[j])));
+                        if (c0 + j < p.BN) {
+                            float y = __uint_as_float(v[j]);
+                            if constexpr (MULTI) {
+                                if (bad) {
+                                    const int k = nt * p.BN + c0 + j, a = tok_id(k);
+                                    if (a >= 0) y += nonfinite_products(mp, a, m0 + m, t0 + k, p.out_ld, TRANS);
+                                }
+                            }
+                            Os[(nt * p.BN + c0 + j) * TM + m] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+                        }
                 }
             }
             asm volatile("bar.sync 1, %0;" ::"n"(C::kDecThreads) : "memory");
@@ -374,6 +601,20 @@ static EncodeTiledFn encode_fn() {
             fn = reinterpret_cast<EncodeTiledFn>(p);
     }
     return fn;
+}
+
+// 3D map over a row-major bf16 [outer][mid][inner] array, boxes of one outer index.
+static bool make_map_3d(CUtensorMap *m, const void *base, uint64_t inner, uint64_t mid, uint64_t outer,
+                        uint32_t box_inner, uint32_t box_mid) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {inner, mid, outer};
+    cuuint64_t strides[2] = {inner * 2, inner * mid * 2};
+    cuuint32_t box[3] = {box_inner, box_mid, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // 2D map over a row-major [outer][inner] array.
@@ -437,15 +678,30 @@ static TileShape choose_shape(int64_t M, int64_t K, int64_t n, int num_sms) {
     return best;
 }
 
-template <bool TRANS, int MT, int NT>
+template <bool TRANS, int MT, int NT, bool MULTI>
 static cudaError_t launch_t(const CUtensorMap &m_codes, const CUtensorMap &m_act, const CUtensorMap &m_lw,
-                            const CUtensorMap &m_lact, const Params &p, dim3 grid, cudaStream_t st) {
+                            const CUtensorMap &m_lact, const Params &p, const MultiParams &mp, dim3 grid, cudaStream_t st) {
     using C = Cfg<MT, NT>;
-    cudaError_t e = cudaFuncSetAttribute(nf4_tc_gemm_kernel<TRANS, MT, NT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmemBytes);
+    constexpr uint32_t smem = MULTI ? C::kSmemBytesMulti : C::kSmemBytes;
+    cudaError_t e = cudaFuncSetAttribute(nf4_tc_gemm_kernel<TRANS, MT, NT, MULTI>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return qln::launch_pdl(nf4_tc_gemm_kernel<TRANS, MT, NT>, grid, dim3(C::kThreads), (size_t)C::kSmemBytes, st,
-                           m_codes, m_act, m_lw, m_lact, p);
+    return qln::launch_pdl(nf4_tc_gemm_kernel<TRANS, MT, NT, MULTI>, grid, dim3(C::kThreads), (size_t)smem, st,
+                           m_codes, m_act, m_lw, m_lact, p, mp);
+}
+
+template <bool MULTI>
+static cudaError_t launch_shape(bool trans, const TileShape &sh, const CUtensorMap &m_codes, const CUtensorMap &m_act,
+                                const CUtensorMap &m_lw, const CUtensorMap &m_lact, const Params &p,
+                                const MultiParams &mp, dim3 grid, cudaStream_t st) {
+    if (trans) {
+        if (sh.MT == 2) return launch_t<true, 2, 1, MULTI>(m_codes, m_act, m_lw, m_lact, p, mp, grid, st);
+        if (sh.NT == 2) return launch_t<true, 1, 2, MULTI>(m_codes, m_act, m_lw, m_lact, p, mp, grid, st);
+        return launch_t<true, 1, 1, MULTI>(m_codes, m_act, m_lw, m_lact, p, mp, grid, st);
+    }
+    if (sh.MT == 2) return launch_t<false, 2, 1, MULTI>(m_codes, m_act, m_lw, m_lact, p, mp, grid, st);
+    if (sh.NT == 2) return launch_t<false, 1, 2, MULTI>(m_codes, m_act, m_lw, m_lact, p, mp, grid, st);
+    return launch_t<false, 1, 1, MULTI>(m_codes, m_act, m_lw, m_lact, p, mp, grid, st);
 }
 
 }  // namespace tc
@@ -465,16 +721,17 @@ int64_t nf4_tc_gemm_ctas(const qln_nf4_weight *w, bool trans, int64_t n, int r, 
     return ((n + (int64_t)shape.NT * shape.BN - 1) / ((int64_t)shape.NT * shape.BN)) * (M / (tc::kBM * shape.MT));
 }
 
-cudaError_t launch_nf4_tc_gemm(const qln_nf4_weight *w, bool trans, const uint16_t *act, int64_t n,
-                               const uint16_t *lact, const uint16_t *lw, int r, uint16_t *out, int *status,
-                               cudaStream_t st, int num_sms) {
+// view: null for one adapter [lw as in launch_nf4_mma_gemm], else the pool's (lw its factors' base).
+static cudaError_t launch_tc(const qln_nf4_weight *w, bool trans, const uint16_t *act, int64_t n, const uint16_t *lact,
+                             const uint16_t *lw, int r, const AdapterView *view, uint16_t *out, int *status,
+                             cudaStream_t st, int num_sms) {
     using namespace tc;
     const int64_t rows = w->rows, cols = w->cols;
     const int64_t M = trans ? cols : rows;
     const int64_t K = trans ? rows : cols;
     const TileShape shape = choose_shape(M, K, n, num_sms > 0 ? num_sms : 148);
-    const int MT = shape.MT, NT = shape.NT, BN = shape.BN;
-    const int TM = kBM * MT;
+    const int NT = shape.NT, BN = shape.BN;
+    const int TM = kBM * shape.MT;
     CUtensorMap m_codes, m_act, m_lw, m_lact;
     bool ok = true;
     // codes as bytes [rows][cols/2]
@@ -483,11 +740,17 @@ cudaError_t launch_nf4_tc_gemm(const qln_nf4_weight *w, bool trans, const uint16
     else ok &= make_map(&m_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w->codes, cols / 2, rows, 32, kBK,
                         CU_TENSOR_MAP_SWIZZLE_NONE);
     ok &= make_map(&m_act, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, act, K, n, kBK, BN, CU_TENSOR_MAP_SWIZZLE_128B);
-    if (!trans) ok &= make_map(&m_lw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, lw, r, rows, kBK, TM,
-                               CU_TENSOR_MAP_SWIZZLE_128B);                       // B [rows][r]
-    else ok &= make_map(&m_lw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, lw, cols, r, 64, kBK,
-                        CU_TENSOR_MAP_SWIZZLE_128B);                               // A [r][cols]
-    ok &= make_map(&m_lact, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, lact, r, n, kBK, BN, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (view) {
+        ok &= trans ? make_map_3d(&m_lw, lw, cols, r, view->count, 64, kBK)    // A [count][r][cols]
+                    : make_map_3d(&m_lw, lw, r, rows, view->count, kBK, TM);   // B [count][rows][r]
+        m_lact = m_act;  // not used
+    } else {
+        if (!trans) ok &= make_map(&m_lw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, lw, r, rows, kBK, TM,
+                                   CU_TENSOR_MAP_SWIZZLE_128B);                       // B [rows][r]
+        else ok &= make_map(&m_lw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, lw, cols, r, 64, kBK,
+                            CU_TENSOR_MAP_SWIZZLE_128B);                               // A [r][cols]
+        ok &= make_map(&m_lact, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, lact, r, n, kBK, BN, CU_TENSOR_MAP_SWIZZLE_128B);
+    }
     if (!ok) return cudaErrorInvalidValue;
 
     Params p;
@@ -505,14 +768,21 @@ cudaError_t launch_nf4_tc_gemm(const qln_nf4_weight *w, bool trans, const uint16
     p.RT = (r + kBK - 1) / kBK;
     p.BN = BN;
     dim3 grid((unsigned)((n + (int64_t)NT * BN - 1) / ((int64_t)NT * BN)), (unsigned)(M / TM));
-    if (trans) {
-        if (MT == 2) return launch_t<true, 2, 1>(m_codes, m_act, m_lw, m_lact, p, grid, st);
-        if (NT == 2) return launch_t<true, 1, 2>(m_codes, m_act, m_lw, m_lact, p, grid, st);
-        return launch_t<true, 1, 1>(m_codes, m_act, m_lw, m_lact, p, grid, st);
-    }
-    if (MT == 2) return launch_t<false, 2, 1>(m_codes, m_act, m_lw, m_lact, p, grid, st);
-    if (NT == 2) return launch_t<false, 1, 2>(m_codes, m_act, m_lw, m_lact, p, grid, st);
-    return launch_t<false, 1, 1>(m_codes, m_act, m_lw, m_lact, p, grid, st);
+    if (!view) return launch_shape<false>(trans, shape, m_codes, m_act, m_lw, m_lact, p, MultiParams{}, grid, st);
+    const MultiParams mp{view->ids, view->rank, lact, lw, view->count, r};
+    return launch_shape<true>(trans, shape, m_codes, m_act, m_lw, m_lact, p, mp, grid, st);
+}
+
+cudaError_t launch_nf4_tc_gemm(const qln_nf4_weight *w, bool trans, const uint16_t *act, int64_t n,
+                               const uint16_t *lact, const uint16_t *lw, int r, uint16_t *out, int *status,
+                               cudaStream_t st, int num_sms) {
+    return launch_tc(w, trans, act, n, lact, lw, r, nullptr, out, status, st, num_sms);
+}
+
+cudaError_t launch_nf4_tc_gemm_multi(const qln_nf4_weight *w, bool trans, const uint16_t *act, int64_t n,
+                                     const uint16_t *lact, const uint16_t *lw, int r, const AdapterView &v,
+                                     uint16_t *out, int *status, cudaStream_t st, int num_sms) {
+    return launch_tc(w, trans, act, n, lact, lw, r, &v, out, status, st, num_sms);
 }
 
 }  // namespace qln

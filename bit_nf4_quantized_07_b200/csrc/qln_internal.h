@@ -157,6 +157,9 @@ cudaError_t launch_nf4_decode_fwd(const qln_nf4_weight *w, const uint16_t *X, in
 cudaError_t launch_nf4_tc_gemm(const qln_nf4_weight *w, bool trans, const uint16_t *act, int64_t n,
                                const uint16_t *lact, const uint16_t *lw, int r, uint16_t *out,
                                int *status, cudaStream_t st, int num_sms);
+cudaError_t launch_nf4_tc_gemm_multi(const qln_nf4_weight *w, bool trans, const uint16_t *act, int64_t n,
+                                     const uint16_t *lact, const uint16_t *lw, int r, const AdapterView &v,
+                                     uint16_t *out, int *status, cudaStream_t st, int num_sms);
 bool nf4_tc_gemm_supported(const qln_nf4_weight *w, bool trans, int64_t n, int r);
 
 }  // namespace qln
