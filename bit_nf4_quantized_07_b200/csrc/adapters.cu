@@ -18,9 +18,10 @@ namespace qln {
 
 // ===========================================================================
 // Plan: a stable counting sort of the tokens by adapter, in one CTA.
-//   order [n]         tokens of adapter 0, then 1, ... (ascending within one)
-//   start [count + 1] first place of each adapter in order
-//   tiles [count + 1] first 64-token tile of each adapter (tiles never mix)
+//   order [n]         tokens of adapter 0, then 1, ... (ascending within one),
+//                     and at the end those without an adapter (group `count`)
+//   start [count + 2] first place of each group in order
+//   tiles [count + 2] first 64-token tile of each group (tiles never mix)
 // Warp w owns the w-th of 32 contiguous token ranges and a histogram of its
 // own, so places follow from two passes over the ids and one scan, and do not
 // depend on timing.  Latency-bound: a few dependent reads of the ids.
@@ -32,7 +33,7 @@ __global__ void __launch_bounds__(kPlanWarps * 32) adapter_plan_kernel(const int
                                                                        int32_t *__restrict__ start,
                                                                        int32_t *__restrict__ tiles, int *status) {
     extern __shared__ int hist[];  // [warp][count]
-    __shared__ int wsum[2][kPlanWarps];
+    __shared__ int wsum[2][kPlanWarps], s_none[kPlanWarps];
     pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -40,10 +41,15 @@ __global__ void __launch_bounds__(kPlanWarps * 32) adapter_plan_kernel(const int
     for (int i = tid; i < kPlanWarps * count; i += kPlanWarps * 32) hist[i] = 0;
     __syncthreads();
     const int t0 = (int)((int64_t)n * warp / kPlanWarps), t1 = (int)((int64_t)n * (warp + 1) / kPlanWarps);
-    for (int t = t0 + lane; t < t1; t += 32) {
-        const int a = __ldg(ids + t);
-        if ((unsigned)a < (unsigned)count) atomicAdd(&hist[warp * count + a], 1);  // a count: order plays no part
+    int none = 0;  // tokens of this warp's range without an adapter
+    for (int tb = t0; tb < t1; tb += 32) {
+        const int t = tb + lane;
+        const int a = t < t1 ? __ldg(ids + t) : 0;
+        const bool in = (unsigned)a < (unsigned)count;
+        if (in && t < t1) atomicAdd(&hist[warp * count + a], 1);  // a count: order plays no part
+        none += __popc(__ballot_sync(0xffffffffu, !in));
     }
+    if (lane == 0) s_none[warp] = none;
     __syncthreads();
     // thread a: this adapter's places within the warps' ranges, and its total
     int total = 0;
@@ -72,32 +78,42 @@ __global__ void __launch_bounds__(kPlanWarps * 32) adapter_plan_kernel(const int
         for (int w = 0; w < warp; ++w) base += wsum[q][w];
         inc[q] += base - v[q];  // exclusive
     }
+    int nall = 0, nbase = 0;  // tokens without an adapter: all, and of the warps before this one
+    for (int w = 0; w < kPlanWarps; ++w) {
+        nbase += w < warp ? s_none[w] : 0;
+        nall += s_none[w];
+    }
     if (tid < count) {
         start[tid] = inc[0];
         tiles[tid] = inc[1];
         if (tid == count - 1) {
             start[count] = inc[0] + v[0];
+            start[count + 1] = n;
             tiles[count] = inc[1] + v[1];
+            tiles[count + 1] = inc[1] + v[1] + ((nall + 63) >> 6);
         }
         for (int w = 0; w < kPlanWarps; ++w) hist[w * count + tid] += inc[0];
     }
     __syncthreads();
+    int at_none = n - nall + nbase;
     for (int tb = t0; tb < t1; tb += 32) {
         const int t = tb + lane;
-        const int a = t < t1 ? __ldg(ids + t) : -1;
-        const bool in = (unsigned)a < (unsigned)count;
+        const int a = t < t1 ? __ldg(ids + t) : 0;
+        const bool in = t < t1 && (unsigned)a < (unsigned)count, out = t < t1 && !in;
         const uint32_t same = __match_any_sync(0xffffffffu, in ? a : -1);
-        const int before = __popc(same & ((1u << lane) - 1u));
-        if (in) order[hist[warp * count + a] + before] = t;
+        const uint32_t below = (1u << lane) - 1u, outs = __ballot_sync(0xffffffffu, out);
+        if (in) order[hist[warp * count + a] + __popc(same & below)] = t;
+        if (out) order[at_none + __popc(outs & below)] = t;
+        at_none += __popc(outs);
         __syncwarp();
-        if (in && before == 0) hist[warp * count + a] += __popc(same);
+        if (in && (same & below) == 0) hist[warp * count + a] += __popc(same);
         __syncwarp();
     }
 }
 
-// The adapter whose tiles hold tile i: tiles[a] <= i < tiles[a + 1].
+// The group whose tiles hold tile i: tiles[a] <= i < tiles[a + 1].
 __device__ __forceinline__ int tile_adapter(const int32_t *tiles, int count, int i) {
-    int lo = 0, hi = count;
+    int lo = 0, hi = count + 1;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (__ldg(tiles + mid) <= i) lo = mid;
@@ -112,61 +128,107 @@ __device__ __forceinline__ int adapter_rank(const int32_t *rank, int a, int r) {
     return k < 0 ? 0 : (k > r ? r : k);
 }
 
+// ---- clusters ------------------------------------------------------------------
+__device__ __forceinline__ void ad_cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ad_peer_f32(uint32_t saddr, uint32_t rank) {
+    uint32_t d;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(saddr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(d) : "memory");
+    return v;
+}
+
+// v as a sum of three bf16 values (24 bits of mantissa, what v holds): the
+// operand of the fp32 gradients.  What a non-finite v leaves is dropped, so
+// that an infinity stays one.
+__device__ __forceinline__ void split3(float v, uint16_t (&q)[3]) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const __nv_bfloat16 h = __float2bfloat16_rn(v);
+        q[k] = __bfloat16_as_ushort(h);
+        v = __fsub_rn(v, __bfloat162float(h));
+        if (!isfinite(v)) v = 0.f;
+    }
+}
+
 // ===========================================================================
-// Down product: partial[split][t][j] = sum over a K range of in[t][k] f_a(j, k),
-// f_a = A_a [r][K] (WKM = false) or B_a [K][r] (WKM = true).  A CTA owns a tile
-// of up to 64 tokens of one adapter (gathered rows) x all r columns x one of
-// the K ranges, streamed through a 4-stage cp.async ring; 4 warps x 16 tokens.
-// HBM-bound: the activations are read once, each adapter once per tile.
+// Down product: v[t][j] = sum_k in[t][k] f_a(j, k), f_a = A_a [r][K] (WKM =
+// false) or B_a [K][r] (WKM = true).  A cluster of 8 CTAs owns a tile of up to
+// 64 tokens of one adapter (gathered rows) x all r columns; each CTA takes an
+// eighth of K, streamed through a 4-stage cp.async ring, 4 warps x 16 tokens;
+// the eight partial tiles meet in shared memory and are added in the order of
+// the CTAs, each CTA finishing 8 tokens.  HBM-bound: the activations are read
+// once, each adapter once per tile, and nothing is written but the result.
+// The tensor cores' running sums move into fp32 registers every 8 chunks of 64
+// (their additions truncate, and the error would grow with K).
+// Results: fp32 (full), bf16(s v) for the GEMM (scaled: its product is rounded
+// to bf16 anyway), and three bf16 parts for the gradients (split, planes of
+// n * r); each may be null.  Zero past an adapter's rank.  Tokens without an
+// adapter get zeros in full only (nothing else of them is read).  With `aux`,
+// its rows (an fp32 [n][r]) are split into aux_split along the way.
 // ===========================================================================
-constexpr int kAdStages = 4;
+constexpr int kAdStages = 4, kAdFlush = 8, kAdCluster = 8;
 constexpr int kAdLd = 72;  // padded row (bf16) of the staged tiles
 
+struct DownArgs {
+    const uint16_t *in, *pool;
+    int64_t n, K;
+    int r, count;
+    const int32_t *order, *start, *tiles, *rank;
+    const float *scale;
+    float *full;
+    uint16_t *scaled, *split;
+    const float *aux;
+    uint16_t *aux_split;
+};
+
 template <int NT, bool WKM>
-__global__ void __launch_bounds__(128) adapter_down_kernel(const uint16_t *__restrict__ in, int64_t n, int64_t K,
-                                                           const uint16_t *__restrict__ pool, int r, int count, int cps,
-                                                           const int32_t *__restrict__ order,
-                                                           const int32_t *__restrict__ start,
-                                                           const int32_t *__restrict__ tiles,
-                                                           float *__restrict__ partial) {
+__global__ void __launch_bounds__(128) adapter_down_kernel(const DownArgs p) {
     extern __shared__ __align__(16) uint16_t dsm[];
     constexpr int WR = NT * 8;
     constexpr int WKLD = WR + 8;
     constexpr int STAGE = 64 * kAdLd + (WKM ? 64 * WKLD : WR * kAdLd);
     pdl_wait();
     pdl_trigger();
-    const int tile = blockIdx.x;
-    if (tile >= __ldg(tiles + count)) return;
-    const int a = tile_adapter(tiles, count, tile);
-    const int p0 = __ldg(start + a) + 64 * (tile - __ldg(tiles + a));
-    const int rows = min(64, __ldg(start + a + 1) - p0);
-    const uint16_t *wt = pool + (int64_t)a * r * K;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tile = blockIdx.x, count = p.count, r = p.r;
+    const int64_t n = p.n, K = p.K;
+    if (tile >= __ldg(p.tiles + count + 1)) return;  // the whole cluster
+    const int a = tile_adapter(p.tiles, count, tile);
+    const int p0 = __ldg(p.start + a) + 64 * (tile - __ldg(p.tiles + a));
+    const int rows = min(64, __ldg(p.start + a + 1) - p0);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, part = blockIdx.y;
+    if (a == count) {  // tokens without an adapter: an eighth of the rows per CTA
+        if (p.full)
+            for (int i = tid; i < 8 * r; i += 128)
+                if (8 * part + i / r < rows) p.full[(int64_t)__ldg(p.order + p0 + 8 * part + i / r) * r + i % r] = 0.f;
+        return;
+    }
+    const uint16_t *wt = p.pool + (int64_t)a * r * K;
     const int g = lane >> 2, c = lane & 3;
-    const int split = blockIdx.y;
-    const int64_t nch = K / 64;
-    const int64_t ch0 = (int64_t)split * cps;
-    const int64_t ch1 = ch0 + cps < nch ? ch0 + cps : nch;
+    const int nch = (int)(K / 64);
+    const int ch0 = nch * part / kAdCluster, ch1 = nch * (part + 1) / kAdCluster;
 
     const uint16_t *src[4];  // this thread's four token rows of a stage (null: a row past the tile)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int row = (tid + 128 * i) >> 3;
-        src[i] = row < rows ? in + (int64_t)__ldg(order + p0 + row) * K + 8 * (tid & 7) : nullptr;
+        src[i] = row < rows ? p.in + (int64_t)__ldg(p.order + p0 + row) * K + 8 * (tid & 7) : nullptr;
     }
-    float acc[NT][4];
+    float acc[NT][4], sum[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
+        for (int e = 0; e < 4; ++e) acc[nt][e] = sum[nt][e] = 0.f;
 
-    auto load = [&](int stage, int64_t ch) {
+    auto load = [&](int stage, int ch) {
         uint16_t *Xs = dsm + stage * STAGE;
         uint16_t *Ws = Xs + 64 * kAdLd;
-        const int64_t k0 = ch * 64;
+        const int64_t k0 = (int64_t)ch * 64;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            cp_async16_zfill(Xs + ((tid + 128 * i) >> 3) * kAdLd + 8 * (tid & 7), src[i] ? src[i] + k0 : in, src[i] ? 16 : 0);
+            cp_async16_zfill(Xs + ((tid + 128 * i) >> 3) * kAdLd + 8 * (tid & 7), src[i] ? src[i] + k0 : p.in, src[i] ? 16 : 0);
         if (WKM) {
             for (int idx = tid; idx < 64 * (WR / 8); idx += 128) {
                 const int row = idx / (WR / 8), ck = idx % (WR / 8);
@@ -181,15 +243,24 @@ __global__ void __launch_bounds__(128) adapter_down_kernel(const uint16_t *__res
             }
         }
     };
+    auto flush = [&]() {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sum[nt][e] = __fadd_rn(sum[nt][e], acc[nt][e]);
+                acc[nt][e] = 0.f;
+            }
+    };
 #pragma unroll
     for (int i = 0; i < kAdStages - 1; ++i) {
         if (ch0 + i < ch1) load(i, ch0 + i);
         cp_async_commit();
     }
-    for (int64_t ch = ch0; ch < ch1; ++ch) {
-        const int it = (int)(ch - ch0);
+    for (int ch = ch0; ch < ch1; ++ch) {
+        const int it = ch - ch0;
         {
-            const int64_t nx = ch + kAdStages - 1;
+            const int nx = ch + kAdStages - 1;
             if (nx < ch1) load((it + kAdStages - 1) % kAdStages, nx);
             cp_async_commit();
         }
@@ -222,99 +293,103 @@ __global__ void __launch_bounds__(128) adapter_down_kernel(const uint16_t *__res
                 mma_bf16_16816(acc[NT - 1], af, b0);
             }
         }
+        if (it % kAdFlush == kAdFlush - 1) flush();
         __syncthreads();
     }
     cp_async_wait<0>();
-    float *dst = partial + (int64_t)split * n * r;
+    flush();
+    // this CTA's partial tile [64][WR + 4], for the cluster
+    constexpr int PLD = WR + 4;
+    float *part_s = reinterpret_cast<float *>(dsm);
+    __syncthreads();
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int row = 16 * warp + g + 8 * h;
-        if (row >= rows) continue;
-        const int64_t t = __ldg(order + p0 + row);
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int j = 8 * nt + 2 * c;
-            if (j < r) *reinterpret_cast<float2 *>(dst + t * r + j) = make_float2(acc[nt][2 * h], acc[nt][2 * h + 1]);
+        for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<float2 *>(part_s + (16 * warp + g + 8 * h) * PLD + 8 * nt + 2 * c) =
+                make_float2(sum[nt][2 * h], sum[nt][2 * h + 1]);
+    ad_cluster_sync();
+    const int rk = adapter_rank(p.rank, a, r);
+    const float s = __ldg(p.scale + a);
+    const uint32_t base = smem_u32(part_s);
+    const int64_t plane = n * r;
+    for (int i = tid; i < 8 * r; i += 128) {  // 8 tokens x r columns per CTA
+        const int row = 8 * part + i / r, j = i % r;
+        if (row >= rows) break;
+        float x[kAdCluster], v = 0.f;
+#pragma unroll
+        for (int q = 0; q < kAdCluster; ++q) x[q] = ad_peer_f32(base + (uint32_t)(row * PLD + j) * 4u, q);
+#pragma unroll
+        for (int q = 0; q < kAdCluster; ++q) v = __fadd_rn(v, x[q]);
+        if (j >= rk) v = 0.f;
+        const int64_t at = (int64_t)__ldg(p.order + p0 + row) * r + j;
+        if (p.full) p.full[at] = v;
+        if (p.scaled) p.scaled[at] = __bfloat16_as_ushort(__float2bfloat16_rn(__fmul_rn(s, v)));
+        uint16_t q3[3];
+        if (p.split) {
+            split3(v, q3);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) p.split[k * plane + at] = q3[k];
+        }
+        if (p.aux_split) {
+            split3(j < rk ? p.aux[at] : 0.f, q3);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) p.aux_split[k * plane + at] = q3[k];
         }
     }
-}
-
-// Sum of the K splits in their order, for token t and column j; zero for a
-// token without an adapter and a column past its adapter's rank.  Written as
-// fp32 (full), as bf16(s v) for the tensor cores (scaled: the operand of a
-// product whose result is rounded to bf16 anyway), and as the pair hi + lo of
-// bf16 values that holds v to 2^-17 (the operand of the fp32 gradients); any
-// of them may be null.
-__global__ void adapter_fold_kernel(const float *__restrict__ partial, int splits, int64_t n, int r,
-                                    const int32_t *__restrict__ ids, int count, const int32_t *__restrict__ rank,
-                                    const float *__restrict__ scale, float *__restrict__ full,
-                                    uint16_t *__restrict__ scaled, uint16_t *__restrict__ hi, uint16_t *__restrict__ lo) {
-    pdl_wait();
-    pdl_trigger();
-    const int64_t total = n * r, stride = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += stride) {
-        const int64_t t = i / r;
-        const int j = (int)(i - t * r), a = __ldg(ids + t);
-        float v = 0.f, s = 0.f;
-        if ((unsigned)a < (unsigned)count && j < adapter_rank(rank, a, r)) {
-            for (int z0 = 0; z0 < splits; z0 += 8) {  // eight loads ahead of their adds
-                float x[8];
-#pragma unroll
-                for (int u = 0; u < 8; ++u) x[u] = z0 + u < splits ? __ldcg(partial + (int64_t)(z0 + u) * total + i) : 0.f;
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    if (z0 + u < splits) v = __fadd_rn(v, x[u]);
-            }
-            s = __ldg(scale + a);
-        }
-        if (full) full[i] = v;
-        if (scaled) scaled[i] = __bfloat16_as_ushort(__float2bfloat16_rn(__fmul_rn(s, v)));
-        if (hi) {
-            const __nv_bfloat16 h = __float2bfloat16_rn(v);
-            const float rest = __fsub_rn(v, __bfloat162float(h));
-            hi[i] = __bfloat16_as_ushort(h);
-            lo[i] = __bfloat16_as_ushort(__float2bfloat16_rn(isfinite(rest) ? rest : 0.f));  // inf - inf
-        }
-    }
+    __syncwarp();
+    ad_cluster_sync();  // no CTA ends while another reads its tile
 }
 
 // ===========================================================================
 // Gradients of the factors: C[m][j] = s_a sum_{t of a} P[t][m] Q[t][j], P = dY
 // and Q = U (dB_a [dout][r]), or P = X and Q = G (dA_a, stored transposed,
-// [r][din]).  A CTA owns 128 m x up to 64 j of one adapter over all of its
-// tokens (gathered rows, steps of 32, 4-stage ring): no splits and no partial
-// sums in memory, one order of every sum.  Q enters as hi + lo, two MMAs each,
-// so that the fp32 result is good to fp32-like accuracy (2^-17 per factor); the
-// tensor cores' running sums are moved into fp32 registers every 512 tokens,
-// so that their truncation does not grow with the sequence.  Adapters without
-// tokens get zeros, and so do columns past an adapter's rank.
+// [r][din]).  A cluster of 4 CTAs owns 128 m x up to 64 j of one adapter; its
+// CTAs take the adapter's 32-token steps in turn (gathered rows, a cp.async
+// ring), so that one long sequence does not leave a single CTA at work, and add
+// their tiles in the order of the CTAs through shared memory.  HBM-bound: every
+// activation is read once (per 64 columns), nothing is written but the result,
+// and the order of every sum is fixed.  Q enters as three bf16 parts, three
+// MMAs each, so that the fp32 result keeps fp32 accuracy; running sums move into
+// fp32 registers every 512 tokens.  Adapters without tokens get zeros, and so
+// do columns past an adapter's rank.
 // ===========================================================================
-constexpr int kAgBM = 128, kAgBK = 32, kAgPad = 136, kAgStages = 4, kAgFlush = 16;
+constexpr int kAgBM = 128, kAgBK = 32, kAgPad = 136, kAgStages = 4, kAgFlush = 16, kAgCluster = 4;
 
 struct GradArgs {
-    const uint16_t *P[2], *Qhi[2], *Qlo[2];  // 0: dB, 1: dA
+    const uint16_t *P[2], *Q[2];  // 0: dB, 1: dA; Q: three planes of n * r
     int64_t M[2];
     float *C[2];
     const int32_t *order, *start, *rank;
     const float *scale;
-    int r, tilesB;
+    int64_t plane;
+    int r, tilesB, jchunks;
 };
 
 template <int NTJ>  // 8 NTJ columns
 __global__ void __launch_bounds__(128) adapter_grad_kernel(const GradArgs p) {
     extern __shared__ __align__(16) uint16_t sk[];
     constexpr int QW = NTJ * 8, QLD = QW + 8;
-    constexpr int STAGE = kAgBK * (kAgPad + 2 * QLD);
+    constexpr int STAGE = kAgBK * (kAgPad + 3 * QLD);
+    constexpr int PLD = QW + 4;  // padded row (fp32) of the partial tile
+    static_assert(kAgBM * PLD * 4 <= kAgStages * STAGE * 2, "the partial tile fits into the ring");
+    __shared__ int s_row[2][kAgBK];  // tokens of a step, read one step ahead
     pdl_wait();
     pdl_trigger();
-    const int which = (int)blockIdx.x < p.tilesB ? 0 : 1;
-    const int a = blockIdx.y, j0 = blockIdx.z * QW, r = p.r;
-    const int64_t M = p.M[which], m0 = (int64_t)((int)blockIdx.x - (which ? p.tilesB : 0)) * kAgBM;
-    const uint16_t *P = p.P[which], *Qh = p.Qhi[which], *Ql = p.Qlo[which];
+    const int mtile = blockIdx.y / p.jchunks, j0 = (int)(blockIdx.y % p.jchunks) * QW;
+    const int which = mtile < p.tilesB ? 0 : 1;
+    const int a = blockIdx.z, part = blockIdx.x, r = p.r;
+    const int64_t M = p.M[which], m0 = (int64_t)(mtile - (which ? p.tilesB : 0)) * kAgBM;
+    const uint16_t *P = p.P[which], *Q = p.Q[which];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3, mat = lane >> 3;
     const int p0 = __ldg(p.start + a), cnt = __ldg(p.start + a + 1) - p0;
-    const int steps = (cnt + kAgBK - 1) / kAgBK;
+    const int allsteps = (cnt + kAgBK - 1) / kAgBK;
+    const int steps = allsteps > part ? (allsteps - part + kAgCluster - 1) / kAgCluster : 0;
+    auto token = [&](int step) -> int {  // thread < 32: its token of this CTA's step, or -1
+        const int q = (step * kAgCluster + part) * kAgBK + tid;
+        return step < steps && q < cnt ? __ldg(p.order + p0 + q) : -1;
+    };
 
     float acc[2][NTJ][4], sum[2][NTJ][4];
 #pragma unroll
@@ -324,34 +399,54 @@ __global__ void __launch_bounds__(128) adapter_grad_kernel(const GradArgs p) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[i][j][e] = sum[i][j][e] = 0.f;
 
-    auto load = [&](int buf, int step) {
-        uint16_t *Ps = sk + buf * STAGE, *Hs = Ps + kAgBK * kAgPad, *Ls = Hs + kAgBK * QLD;
+    auto load = [&](int buf, const int *rows) {
+        uint16_t *Ps = sk + buf * STAGE, *Qs = Ps + kAgBK * kAgPad;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // P: 32 rows x 16 chunks
-            const int idx = tid + 128 * i, row = idx >> 4, ck = idx & 15, q = step * kAgBK + row;
+            const int idx = tid + 128 * i, row = idx >> 4, ck = idx & 15, t = rows[row];
             const int64_t col = m0 + 8 * ck;
-            const bool ok = q < cnt && col < M;
-            cp_async16_zfill(Ps + row * kAgPad + 8 * ck, ok ? P + (int64_t)__ldg(p.order + p0 + q) * M + col : P, ok ? 16 : 0);
+            const bool ok = t >= 0 && col < M;
+            cp_async16_zfill(Ps + row * kAgPad + 8 * ck, ok ? P + (int64_t)t * M + col : P, ok ? 16 : 0);
         }
-        for (int idx = tid; idx < 2 * kAgBK * NTJ; idx += 128) {  // Q: 32 rows x NTJ chunks, hi then lo
-            const int h = idx >= kAgBK * NTJ, k = idx - h * kAgBK * NTJ, row = k / NTJ, ck = k % NTJ, q = step * kAgBK + row;
-            const bool ok = q < cnt && j0 + 8 * ck < r;
-            const uint16_t *Q = h ? Ql : Qh;
-            cp_async16_zfill((h ? Ls : Hs) + row * QLD + 8 * ck,
-                             ok ? Q + (int64_t)__ldg(p.order + p0 + q) * r + j0 + 8 * ck : Q, ok ? 16 : 0);
-        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k)  // Q: three parts of 32 rows x NTJ chunks
+            for (int idx = tid; idx < kAgBK * NTJ; idx += 128) {
+                const int row = idx / NTJ, ck = idx % NTJ, t = rows[row];
+                const bool ok = t >= 0 && j0 + 8 * ck < r;
+                cp_async16_zfill(Qs + (k * kAgBK + row) * QLD + 8 * ck,
+                                 ok ? Q + k * p.plane + (int64_t)t * r + j0 + 8 * ck : Q, ok ? 16 : 0);
+            }
     };
+    auto flush = [&]() {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < NTJ; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    sum[i][j][e] = __fadd_rn(sum[i][j][e], acc[i][j][e]);
+                    acc[i][j][e] = 0.f;
+                }
+    };
+    if (tid < kAgBK) s_row[0][tid] = token(0);
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < kAgStages - 1; ++i) {
-        if (i < steps) load(i, i);
+        const int next = tid < kAgBK ? token(i + 1) : 0;
+        load(i, s_row[i & 1]);
         cp_async_commit();
+        if (tid < kAgBK) s_row[(i + 1) & 1][tid] = next;
+        __syncthreads();
     }
     for (int it = 0; it < steps; ++it) {
-        if (it + kAgStages - 1 < steps) load((it + kAgStages - 1) % kAgStages, it + kAgStages - 1);
+        const int nx = it + kAgStages - 1;  // the step loaded now; its tokens are in s_row[nx & 1]
+        const int next = tid < kAgBK ? token(nx + 1) : 0;
+        if (nx < steps) load(nx % kAgStages, s_row[nx & 1]);
         cp_async_commit();
         cp_async_wait<kAgStages - 1>();
+        if (tid < kAgBK) s_row[(nx + 1) & 1][tid] = next;
         __syncthreads();
-        const uint16_t *Ps = sk + (it % kAgStages) * STAGE, *Hs = Ps + kAgBK * kAgPad;
+        const uint16_t *Ps = sk + (it % kAgStages) * STAGE, *Qb = Ps + kAgBK * kAgPad;
 #pragma unroll
         for (int kk = 0; kk < kAgBK; kk += 16) {
             uint32_t af[2][4];
@@ -360,8 +455,8 @@ __global__ void __launch_bounds__(128) adapter_grad_kernel(const GradArgs p) {
                 ldmatrix_x4_trans(af[mt][0], af[mt][1], af[mt][2], af[mt][3],
                                   Ps + (kk + (mat >> 1) * 8 + (lane & 7)) * kAgPad + warp * 32 + mt * 16 + (mat & 1) * 8);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint16_t *Qs = Hs + h * kAgBK * QLD + (kk + (mat & 1) * 8 + (lane & 7)) * QLD;
+            for (int h = 0; h < 3; ++h) {
+                const uint16_t *Qs = Qb + (h * kAgBK + kk + (mat & 1) * 8 + (lane & 7)) * QLD;
 #pragma unroll
                 for (int np = 0; np < NTJ / 2; ++np) {
                     uint32_t r0, r1, r2, r3;
@@ -382,49 +477,55 @@ __global__ void __launch_bounds__(128) adapter_grad_kernel(const GradArgs p) {
                 }
             }
         }
-        if (it % kAgFlush == kAgFlush - 1) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < NTJ; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        sum[i][j][e] = __fadd_rn(sum[i][j][e], acc[i][j][e]);
-                        acc[i][j][e] = 0.f;
-                    }
-        }
+        if (it % kAgFlush == kAgFlush - 1) flush();
         __syncthreads();
     }
     cp_async_wait<0>();
-    const int rk = adapter_rank(p.rank, a, r);
-    const float s = __ldg(p.scale + a);
-    float *C = p.C[which] + (int64_t)a * M * r;
+    flush();
+    float *part_s = reinterpret_cast<float *>(sk);  // this CTA's partial tile [128][PLD]
+    __syncthreads();
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NTJ; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int64_t m = m0 + warp * 32 + mt * 16 + g + 8 * (e >> 1);
-                const int j = j0 + nt * 8 + 2 * c + (e & 1);
-                if (m < M && j < r) {
-                    const float v = cnt > 0 && j < rk ? __fmul_rn(s, __fadd_rn(sum[mt][nt][e], acc[mt][nt][e])) : 0.f;
-                    C[which ? (int64_t)j * M + m : m * r + j] = v;
-                }
-            }
+            for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<float2 *>(part_s + (warp * 32 + mt * 16 + g + 8 * h) * PLD + nt * 8 + 2 * c) =
+                    make_float2(sum[mt][nt][2 * h], sum[mt][nt][2 * h + 1]);
+    ad_cluster_sync();
+    const int rk = cnt > 0 ? adapter_rank(p.rank, a, r) : 0;
+    const float s = __ldg(p.scale + a);
+    const uint32_t base = smem_u32(part_s);
+    float *C = p.C[which] + (int64_t)a * M * r;
+    const int jw = min(QW, r - j0);
+    for (int i = tid; i < 32 * jw; i += 128) {  // 32 m x jw columns per CTA
+        const int m = 32 * part + (which ? i & 31 : i / jw), j = which ? i >> 5 : i % jw;
+        if (m0 + m >= M) continue;
+        float x[kAgCluster], v = 0.f;
+#pragma unroll
+        for (int q = 0; q < kAgCluster; ++q) x[q] = ad_peer_f32(base + (uint32_t)(m * PLD + j) * 4u, q);
+#pragma unroll
+        for (int q = 0; q < kAgCluster; ++q) v = __fadd_rn(v, x[q]);
+        v = j0 + j < rk ? __fmul_rn(s, v) : 0.f;
+        C[which ? (int64_t)(j0 + j) * M + m0 + m : (m0 + m) * r + j0 + j] = v;
+    }
+    __syncwarp();
+    ad_cluster_sync();  // no CTA ends while another reads its tile
 }
 
 // ---- host --------------------------------------------------------------------
 static size_t r256(size_t x) { return (x + 255) & ~size_t(255); }
 
-size_t adapter_plan_bytes(int64_t n) { return r256((size_t)n * 4) + 2 * r256((QLN_MAX_ADAPTERS + 1) * 4); }
+static size_t plan_table() { return r256((QLN_MAX_ADAPTERS + 2) * 4); }
+
+size_t adapter_plan_bytes(int64_t n) { return r256((size_t)n * 4) + 2 * plan_table(); }
 
 AdapterPlan adapter_plan_at(void *base, int64_t n) {
     char *b = static_cast<char *>(base);
     AdapterPlan p;
     p.order = reinterpret_cast<int32_t *>(b);
     p.start = reinterpret_cast<int32_t *>(b + r256((size_t)n * 4));
-    p.tiles = reinterpret_cast<int32_t *>(b + r256((size_t)n * 4) + r256((QLN_MAX_ADAPTERS + 1) * 4));
+    p.tiles = reinterpret_cast<int32_t *>(b + r256((size_t)n * 4) + plan_table());
     return p;
 }
 
@@ -438,64 +539,75 @@ cudaError_t launch_adapter_plan(const int32_t *ids, int64_t n, int count, const 
                       p.tiles, status);
 }
 
-template <int NT, bool WKM>
-static cudaError_t launch_ad_down(const uint16_t *in, int64_t n, int64_t K, const uint16_t *pool, int r, int count,
-                                  const AdapterPlan &p, int splits, int cps, float *partial, cudaStream_t st) {
-    constexpr size_t smem = (size_t)kAdStages * (64 * kAdLd + (WKM ? 64 * (NT * 8 + 8) : NT * 8 * kAdLd)) * sizeof(uint16_t);
-    auto kern = adapter_down_kernel<NT, WKM>;
+// launch_pdl with a thread-block cluster.
+template <typename Args>
+static cudaError_t launch_cluster(void (*kernel)(const Args), dim3 grid, dim3 cluster, size_t smem, cudaStream_t st,
+                                  const Args &args) {
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    // every adapter's last tile may be partial: at most n / 64 whole tiles and one more per adapter present
-    const int64_t tiles = n / 64 + (count < n ? count : n);
-    return launch_pdl(kern, dim3((unsigned)tiles, (unsigned)splits), dim3(128), smem, st, in, n, K, pool, r, count, cps,
-                      (const int32_t *)p.order, (const int32_t *)p.start, (const int32_t *)p.tiles, partial);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster.x;
+    attr[0].val.clusterDim.y = cluster.y;
+    attr[0].val.clusterDim.z = cluster.z;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    note_launch();
+    return cudaLaunchKernelEx(&cfg, kernel, args);
 }
 
-cudaError_t launch_adapter_down(const uint16_t *in, int64_t n, int64_t K, const uint16_t *pool, bool kmajor, int r,
-                                int count, const AdapterPlan &p, float *partial, int splits, int cps, cudaStream_t st) {
-#define QLN_AD_DOWN(NT) \
-    (kmajor ? launch_ad_down<NT, true>(in, n, K, pool, r, count, p, splits, cps, partial, st) \
-            : launch_ad_down<NT, false>(in, n, K, pool, r, count, p, splits, cps, partial, st))
-    if (r <= 8) return QLN_AD_DOWN(1);
-    if (r <= 16) return QLN_AD_DOWN(2);
-    if (r <= 32) return QLN_AD_DOWN(4);
-    if (r <= 64) return QLN_AD_DOWN(8);
+template <int NT, bool WKM>
+static cudaError_t launch_ad_down(const DownArgs &a, cudaStream_t st) {
+    constexpr size_t smem = (size_t)kAdStages * (64 * kAdLd + (WKM ? 64 * (NT * 8 + 8) : NT * 8 * kAdLd)) * sizeof(uint16_t);
+    static_assert(smem >= 64 * (NT * 8 + 4) * 4, "the partial tile fits into the ring");
+    // every group's last tile may be partial: at most n / 64 whole tiles and one more per group present
+    const int64_t tiles = a.n / 64 + (a.count + 1 < a.n ? a.count + 1 : a.n);
+    return launch_cluster(adapter_down_kernel<NT, WKM>, dim3((unsigned)tiles, kAdCluster), dim3(1, kAdCluster), smem, st, a);
+}
+
+cudaError_t launch_adapter_down(const uint16_t *in, int64_t n, int64_t K, const qln_adapter_pool *pool, bool kmajor,
+                                const AdapterPlan &p, float *full, uint16_t *scaled, uint16_t *split, const float *aux,
+                                uint16_t *aux_split, cudaStream_t st) {
+    const DownArgs a{in, kmajor ? pool->B : pool->A, n, K, pool->r, pool->count, p.order, p.start, p.tiles, pool->rank,
+                     pool->scale, full, scaled, split, aux, aux_split};
+#define QLN_AD_DOWN(NT) (kmajor ? launch_ad_down<NT, true>(a, st) : launch_ad_down<NT, false>(a, st))
+    if (a.r <= 8) return QLN_AD_DOWN(1);
+    if (a.r <= 16) return QLN_AD_DOWN(2);
+    if (a.r <= 32) return QLN_AD_DOWN(4);
+    if (a.r <= 64) return QLN_AD_DOWN(8);
     return QLN_AD_DOWN(16);
 #undef QLN_AD_DOWN
 }
 
-cudaError_t launch_adapter_fold(const float *partial, int splits, int64_t n, const qln_adapter_pool *pool,
-                                const int32_t *ids, float *full, uint16_t *scaled, uint16_t *hi, uint16_t *lo, cudaStream_t st) {
-    int64_t blocks = (n * pool->r + 255) / 256;
-    if (blocks > 2048) blocks = 2048;
-    return launch_pdl(adapter_fold_kernel, dim3((unsigned)blocks), dim3(256), 0, st, partial, splits, n, (int)pool->r, ids,
-                      (int)pool->count, pool->rank, pool->scale, full, scaled, hi, lo);
-}
-
 template <int NTJ>
-static cudaError_t launch_ad_grad(const GradArgs &a, int count, cudaStream_t st) {
-    constexpr size_t smem = (size_t)kAgStages * kAgBK * (kAgPad + 2 * (NTJ * 8 + 8)) * sizeof(uint16_t);
-    auto kern = adapter_grad_kernel<NTJ>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
+static cudaError_t launch_ad_grad(GradArgs &a, int count, cudaStream_t st) {
+    constexpr size_t smem = (size_t)kAgStages * kAgBK * (kAgPad + 3 * (NTJ * 8 + 8)) * sizeof(uint16_t);
     const unsigned tilesA = (unsigned)((a.M[1] + kAgBM - 1) / kAgBM);
-    return launch_pdl(kern, dim3((unsigned)a.tilesB + tilesA, (unsigned)count, (unsigned)((a.r + 8 * NTJ - 1) / (8 * NTJ))),
-                      dim3(128), smem, st, a);
+    a.jchunks = (a.r + 8 * NTJ - 1) / (8 * NTJ);
+    return launch_cluster(adapter_grad_kernel<NTJ>, dim3(kAgCluster, (a.tilesB + tilesA) * a.jchunks, (unsigned)count),
+                          dim3(kAgCluster), smem, st, a);
 }
 
-cudaError_t launch_adapter_grads(const uint16_t *dY, const uint16_t *Uhi, const uint16_t *Ulo, int64_t dout,
-                                 const uint16_t *X, const uint16_t *Ghi, const uint16_t *Glo, int64_t din,
-                                 const qln_adapter_pool *pool, const AdapterPlan &p, float *dA, float *dB, cudaStream_t st) {
+cudaError_t launch_adapter_grads(const uint16_t *dY, const uint16_t *U3, int64_t dout, const uint16_t *X,
+                                 const uint16_t *G3, int64_t din, int64_t n, const qln_adapter_pool *pool,
+                                 const AdapterPlan &p, float *dA, float *dB, cudaStream_t st) {
     GradArgs a;
     a.P[0] = dY, a.P[1] = X;
-    a.Qhi[0] = Uhi, a.Qhi[1] = Ghi;
-    a.Qlo[0] = Ulo, a.Qlo[1] = Glo;
+    a.Q[0] = U3, a.Q[1] = G3;
     a.M[0] = dout, a.M[1] = din;
     a.C[0] = dB, a.C[1] = dA;
     a.order = p.order, a.start = p.start, a.rank = pool->rank;
     a.scale = pool->scale;
+    a.plane = n * pool->r;
     a.r = pool->r;
     a.tilesB = (int)((dout + kAgBM - 1) / kAgBM);
     if (a.r <= 8) return launch_ad_grad<1>(a, pool->count, st);

@@ -123,26 +123,20 @@ qln_status check_linear(const qln_nf4_weight *w, const uint16_t *X, int64_t n, c
 qln_status from_cuda(cudaError_t e) { return e == cudaSuccess ? QLN_OK : QLN_ERR_CUDA; }
 
 // Workspace of the calls with a pool of adapters (offsets 256-byte aligned):
-//   header, plan (order, start, tiles), then
-//   fwd: sU [n][r] bf16, split-K partials of U (fp32)
-//   bwd: sG, G hi, G lo, U hi, U lo [n][r] bf16, split-K partials (fp32)
+//   header, plan (order, start, tiles), s U or s G [n][r] bf16,
+//   bwd: G and U as three bf16 planes [3][n][r] each
 struct MultiWs {
-    size_t plan, scaled, ghi, glo, uhi, ulo, partial, total;
+    size_t plan, scaled, g3, u3, total;
 };
 
-MultiWs multi_layout(bool bwd, int64_t rows, int64_t cols, int64_t n, int r) {
+MultiWs multi_layout(bool bwd, int64_t n, int r) {
     MultiWs L;
-    const size_t nr = round256((size_t)n * r * 2);
+    const size_t nr = (size_t)n * r * 2;
     L.plan = qln::kWsHeaderBytes;
     L.scaled = L.plan + qln::adapter_plan_bytes(n);
-    L.ghi = L.scaled + nr;
-    L.glo = L.ghi + (bwd ? nr : 0);
-    L.uhi = L.glo + (bwd ? nr : 0);
-    L.ulo = L.uhi + (bwd ? nr : 0);
-    L.partial = L.ulo + (bwd ? nr : 0);
-    size_t p = qln::lora_down_partial_bytes(n, cols, r, kSplitTargetSms);
-    const size_t g = bwd ? qln::lora_down_partial_bytes(n, rows, r, kSplitTargetSms) : 0;
-    L.total = L.partial + round256(p > g ? p : g);
+    L.g3 = L.scaled + round256(nr);
+    L.u3 = L.g3 + (bwd ? round256(3 * nr) : 0);
+    L.total = L.u3 + (bwd ? round256(3 * nr) : 0);
     return L;
 }
 
@@ -157,15 +151,6 @@ qln_status check_multi(const qln_nf4_weight *w, const qln_adapter_pool *pool, co
     if (n > kMaxMultiTokens || pool->count < 1 || pool->count > QLN_MAX_ADAPTERS) return QLN_ERR_SHAPE;
     if (!aligned(ids, 4) || !aligned(pool->scale, 4) || !aligned(pool->rank, 4)) return QLN_ERR_ALIGN;
     return QLN_OK;
-}
-
-// in's products down to the rank, as partials per K split; returns the splits.
-cudaError_t multi_down(const uint16_t *in, int64_t n, int64_t K, const uint16_t *factors, bool kmajor,
-                       const qln_adapter_pool *pool, const qln::AdapterPlan &plan, float *partial, int *splits,
-                       cudaStream_t st) {
-    int cps = 0;
-    qln::lora_down_plan(n, K, pool->r, kSplitTargetSms, splits, &cps);
-    return qln::launch_adapter_down(in, n, K, factors, kmajor, pool->r, pool->count, plan, partial, *splits, cps, st);
 }
 
 cudaError_t multi_gemm(const qln_nf4_weight *w, bool trans, const uint16_t *act, int64_t n, const uint16_t *lact,
@@ -482,7 +467,7 @@ qln_status qlora_multi_fwd(const qln_nf4_weight *w, const qln_adapter_pool *pool
     if (st != QLN_OK) return st;
     if (!Y || !ws) return QLN_ERR_NULL;
     if (!aligned(Y, 16) || !aligned(U_out, 16) || !aligned(ws, 256)) return QLN_ERR_ALIGN;
-    const MultiWs L = multi_layout(false, w->rows, w->cols, n, pool->r);
+    const MultiWs L = multi_layout(false, n, pool->r);
     if (ws_bytes < L.total) return QLN_ERR_WORKSPACE;
     int sms = 0;
     st = check_device(&sms);
@@ -491,15 +476,12 @@ qln_status qlora_multi_fwd(const qln_nf4_weight *w, const qln_adapter_pool *pool
     char *wsb = reinterpret_cast<char *>(ws);
     const qln::AdapterPlan plan = qln::adapter_plan_at(wsb + L.plan, n);
     uint16_t *sU = reinterpret_cast<uint16_t *>(wsb + L.scaled);
-    float *partial = reinterpret_cast<float *>(wsb + L.partial);
-    int splits = 0;
-    cudaError_t e = qln::launch_adapter_plan(ids, n, pool->count, plan, reinterpret_cast<int *>(wsb), cs);
+    int *status = reinterpret_cast<int *>(wsb);
+    cudaError_t e = qln::launch_adapter_plan(ids, n, pool->count, plan, status, cs);
     if (e != cudaSuccess) return QLN_ERR_CUDA;
-    e = multi_down(X, n, w->cols, pool->A, false, pool, plan, partial, &splits, cs);
+    e = qln::launch_adapter_down(X, n, w->cols, pool, false, plan, U_out, sU, nullptr, nullptr, nullptr, cs);
     if (e != cudaSuccess) return QLN_ERR_CUDA;
-    e = qln::launch_adapter_fold(partial, splits, n, pool, ids, U_out, sU, nullptr, nullptr, cs);
-    if (e != cudaSuccess) return QLN_ERR_CUDA;
-    return from_cuda(multi_gemm(w, false, X, n, sU, pool->B, pool, ids, Y, reinterpret_cast<int *>(wsb), cs, sms));
+    return from_cuda(multi_gemm(w, false, X, n, sU, pool->B, pool, ids, Y, status, cs, sms));
 }
 
 qln_status qlora_multi_bwd(const qln_nf4_weight *w, const qln_adapter_pool *pool, const uint16_t *X, int64_t n,
@@ -511,7 +493,7 @@ qln_status qlora_multi_bwd(const qln_nf4_weight *w, const qln_adapter_pool *pool
     if (!aligned(dY, 16) || !aligned(U, 16) || !aligned(dX, 16) || !aligned(dA, 16) || !aligned(dB, 16) ||
         !aligned(ws, 256))
         return QLN_ERR_ALIGN;
-    const MultiWs L = multi_layout(true, w->rows, w->cols, n, pool->r);
+    const MultiWs L = multi_layout(true, n, pool->r);
     if (ws_bytes < L.total) return QLN_ERR_WORKSPACE;
     int sms = 0;
     st = check_device(&sms);
@@ -520,28 +502,19 @@ qln_status qlora_multi_bwd(const qln_nf4_weight *w, const qln_adapter_pool *pool
     char *wsb = reinterpret_cast<char *>(ws);
     const qln::AdapterPlan plan = qln::adapter_plan_at(wsb + L.plan, n);
     uint16_t *sG = reinterpret_cast<uint16_t *>(wsb + L.scaled);
-    uint16_t *Ghi = reinterpret_cast<uint16_t *>(wsb + L.ghi), *Glo = reinterpret_cast<uint16_t *>(wsb + L.glo);
-    uint16_t *Uhi = reinterpret_cast<uint16_t *>(wsb + L.uhi), *Ulo = reinterpret_cast<uint16_t *>(wsb + L.ulo);
-    float *partial = reinterpret_cast<float *>(wsb + L.partial);
-    int splits = 0;
-    cudaError_t e = qln::launch_adapter_plan(ids, n, pool->count, plan, reinterpret_cast<int *>(wsb), cs);
+    uint16_t *G3 = reinterpret_cast<uint16_t *>(wsb + L.g3), *U3 = reinterpret_cast<uint16_t *>(wsb + L.u3);
+    int *status = reinterpret_cast<int *>(wsb);
+    cudaError_t e = qln::launch_adapter_plan(ids, n, pool->count, plan, status, cs);
     if (e != cudaSuccess) return QLN_ERR_CUDA;
-    const float *Usrc = U;  // [n][r], or the partials of its recomputation
-    int usplits = 1;
     if (!U) {
-        e = multi_down(X, n, w->cols, pool->A, false, pool, plan, partial, &usplits, cs);
+        e = qln::launch_adapter_down(X, n, w->cols, pool, false, plan, nullptr, nullptr, U3, nullptr, nullptr, cs);
         if (e != cudaSuccess) return QLN_ERR_CUDA;
-        Usrc = partial;
     }
-    e = qln::launch_adapter_fold(Usrc, usplits, n, pool, ids, nullptr, nullptr, Uhi, Ulo, cs);
+    e = qln::launch_adapter_down(dY, n, w->rows, pool, true, plan, nullptr, sG, G3, U, U ? U3 : nullptr, cs);
     if (e != cudaSuccess) return QLN_ERR_CUDA;
-    e = multi_down(dY, n, w->rows, pool->B, true, pool, plan, partial, &splits, cs);
+    e = qln::launch_adapter_grads(dY, U3, w->rows, X, G3, w->cols, n, pool, plan, dA, dB, cs);
     if (e != cudaSuccess) return QLN_ERR_CUDA;
-    e = qln::launch_adapter_fold(partial, splits, n, pool, ids, nullptr, sG, Ghi, Glo, cs);
-    if (e != cudaSuccess) return QLN_ERR_CUDA;
-    e = multi_gemm(w, true, dY, n, sG, pool->A, pool, ids, dX, reinterpret_cast<int *>(wsb), cs, sms);
-    if (e != cudaSuccess) return QLN_ERR_CUDA;
-    return from_cuda(qln::launch_adapter_grads(dY, Uhi, Ulo, w->rows, X, Ghi, Glo, w->cols, pool, plan, dA, dB, cs));
+    return from_cuda(multi_gemm(w, true, dY, n, sG, pool->A, pool, ids, dX, status, cs, sms));
 }
 
 size_t qln_workspace_bytes(int32_t op, int64_t rows, int64_t cols, int64_t n, int32_t r) {
@@ -555,7 +528,7 @@ size_t qln_workspace_bytes(int32_t op, int64_t rows, int64_t cols, int64_t n, in
         case QLN_OP_MULTI_FWD:
         case QLN_OP_MULTI_BWD:
             return (rows > 0 && cols > 0 && n > 0 && n <= kMaxMultiTokens && r > 0)
-                       ? multi_layout(op == QLN_OP_MULTI_BWD, rows, cols, n, r).total
+                       ? multi_layout(op == QLN_OP_MULTI_BWD, n, r).total
                        : 0;
         case QLN_OP_QUANTIZE_DQ_BATCH:
             return (rows > 0 && rows <= kMaxBatchJobs) ? qln::kDqBatchScratchBytes * (size_t)rows : 0;

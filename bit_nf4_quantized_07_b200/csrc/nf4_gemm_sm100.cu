@@ -27,15 +27,20 @@
 // MULTI: each token has an adapter of its own from a pool.  The adapter term
 // takes ceil(rank / 64) k-steps per adapter present among the tile's tokens, in
 // the order of their first tokens (warp 1 lists them while the pipeline
-// fills).  Such a step's A_op is the adapter's factor by TMA (3-D map, so rows
-// past the factor read as zero); its B_op is written by the decoders, s*U or
-// s*G of the adapter's own tokens and zero for the others (all MMAs keep one
-// shape: only then do they run in the order of their issue).  A zero times an
-// infinity would still be a NaN, so the decoders also replace what is not
-// finite in the factor's tile by zero, and the epilogue adds those products
-// to their own tokens one by one (a path that finite factors never take).
-// An adapter step costs as much as a weight step at most; a prefill tile of
-// packed sequences has one or two.
+// fills).  Such a step's A_op is the adapter's factor (3-D map, so rows past
+// the factor read as zero), its B_op s*U or s*G, both by TMA; the decoders then
+// write zeros over the other adapters' tokens.  All MMAs keep one shape: only
+// then do they run in the order of their issue.  A zero times an infinity would
+// still be a NaN, so the decoders also replace what is not finite in the
+// factor's tile by zero, and the epilogue adds those products to their own
+// tokens one by one (a path that finite factors never take).  An adapter step
+// costs as much as a weight step at most; a prefill tile of packed sequences
+// has one or two.
+// A MULTI kernel reads its activations and weights before the kernel ahead of
+// it on the stream has completed, and waits for that one only before the
+// adapter steps.  This is safe because the call's first kernel waits for all
+// earlier work, and every kernel of the call lets its dependents start only
+// after its own wait.
 // Warp roles: warp 0 TMA producer, warp 1 TMEM owner + single-thread MMA
 // issuer, warps 2.. decoders and then the epilogue (TMEM -> BF16 -> HBM).
 // Every barrier wait is bounded; on give-up the CTA records QLN_ERR_TIMEOUT
@@ -176,7 +181,7 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
         tma_prefetch_map(&tm_codes);
         tma_prefetch_map(&tm_act);
         tma_prefetch_map(&tm_lw);
-        if (!MULTI) tma_prefetch_map(&tm_lact);
+        tma_prefetch_map(&tm_lact);
     }
     if (warp == 1) {
         tmem_alloc(smem_addr(tmem_slot), C::kTmemCols);
@@ -188,8 +193,10 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
     const uint32_t tmem_d = *tmem_slot;
     // Barriers, descriptors and TMEM are set up while the previous kernel on
     // the stream finishes; every global access comes after this wait.
-    qln::pdl_wait();
-    qln::pdl_trigger();
+    if (!MULTI) {
+        qln::pdl_wait();
+        qln::pdl_trigger();
+    }
 
     auto give_up = [&]() {
         *abort_flag = 1;
@@ -242,6 +249,8 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                 issued = kt + 1;
             }
             if constexpr (MULTI) {
+                qln::pdl_wait();  // s U or s G is there
+                qln::pdl_trigger();
                 if (issued == nsteps && !mbar_wait_bounded(list_full, 0, abort_flag, kWaitLimitNs)) {
                     give_up();
                 } else if (issued == nsteps) {
@@ -255,7 +264,11 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                                 break;
                             }
                             const uint32_t sA = sbase + C::kOffA + s * C::kABytes;
-                            mbar_arrive_expect_tx(tma_full(s), C::kABytes);
+                            mbar_arrive_expect_tx(tma_full(s), C::kABytes + bbytes);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                tma_load_2d(sbase + C::kOffB + s * C::kBBytes + nt * bsub, &tm_lact, j,
+                                            (int32_t)(t0 + nt * p.BN), tma_full(s));
                             if (!TRANS) {
                                 tma_load_3d(sA, &tm_lw, j, (int32_t)m0, a, tma_full(s));
                             } else {
@@ -469,53 +482,52 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                 for (int j = 0; j < rk; j += kBK, ++kt) {
                     const int s = kt % S;
                     const uint32_t ph = (uint32_t)(kt / S) & 1u;
-                    if (!mbar_wait_bounded(empty(s), ph ^ 1u, abort_flag, kWaitLimitNs)) {
-                        give_up();
-                        break;
-                    }
                     const int left = rk - j < kBK ? rk - j : kBK, cks = 2 * ((left + 15) / 16);  // 8-wide chunks
                     const uint32_t sB = sbase + C::kOffB + s * C::kBBytes;
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const int work = in_sub(e, nt) ? p.BN * cks : 0;
-#pragma unroll 4
-                        for (int i = dt; i < work; i += C::kDecThreads) {
-                            const int row = i / cks, c = i % cks, k = nt * p.BN + row;
-                            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                            if (s_tok[k] == a && j + 8 * c < mp.r)
-                                v = __ldcg(reinterpret_cast<const uint4 *>(mp.lact + (t0 + k) * mp.r + j + 8 * c));
-                            st_shared_v4(sB + (nt * p.BN + row) * 128 + ((c ^ (row & 7)) << 4), v);
-                        }
-                    }
                     if (!mbar_wait_bounded(tma_full(s), ph, abort_flag, kWaitLimitNs)) {
                         give_up();
                         break;
+                    }
+                    for (int nt = 0; nt < NT; ++nt) {
+                        if (!in_sub(e, nt)) continue;
+                        for (int row = dt; row < p.BN; row += C::kDecThreads) {
+                            if (s_tok[nt * p.BN + row] == a) continue;
+                            const uint32_t at = sB + (nt * p.BN + row) * 128;
+                            for (int c = 0; c < cks; ++c)
+                                st_shared_v4(at + ((c ^ (row & 7)) << 4), make_uint4(0u, 0u, 0u, 0u));
+                        }
                     }
                     // The factor's tile: zero past the rank, and where it is not finite.  One thread per
                     // 128-byte row: 64 columns j of one m, or 64 m of one row j.
                     uint8_t *row = smem + C::kOffA + s * C::kABytes + (TRANS ? dcol * 8192 + drow * 128 : dt * 128);
                     const int r7 = (TRANS ? drow : dt) & 7;
-                    const bool past = TRANS && drow >= left;  // the whole row is past the rank
-                    bool bad = false;
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        if (TRANS ? drow >= 8 * cks : c >= cks) continue;  // the MMA does not read it
+                    const int cend = TRANS ? (drow < 8 * cks ? 8 : 0) : cks;  // chunks that the MMA reads
+                    const int keep = TRANS ? (drow < left ? 64 : 0) : left;   // columns before the rank's end
+                    __nv_bfloat162 odd = __float2bfloat162_rn(0.f);           // NaN once an element is not finite
+                    const __nv_bfloat162 zero = odd;
+                    for (int c = 0; c < cend; ++c) {
                         uint4 *q = reinterpret_cast<uint4 *>(row + ((c ^ r7) << 4));
-                        const uint4 v = *q;
-                        uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                        bool fix = false;
+                        uint4 v = *q;
+                        if (8 * c + 8 > keep) {  // (partly) past the rank
+                            uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                        for (int h = 0; h < 8; ++h) {
-                            const uint32_t x = (w[h >> 1] >> (16 * (h & 1))) & 0xffffu;
-                            const bool out = TRANS ? past : 8 * c + h >= left;
-                            const bool inf = (x & 0x7f80u) == 0x7f80u && !out;
-                            bad |= inf;
-                            if ((inf || out) && x) {
-                                w[h >> 1] &= (h & 1) ? 0x0000ffffu : 0xffff0000u;
-                                fix = true;
-                            }
+                            for (int h = 0; h < 8; ++h)
+                                if (8 * c + h >= keep) w[h >> 1] &= (h & 1) ? 0x0000ffffu : 0xffff0000u;
+                            *q = v = make_uint4(w[0], w[1], w[2], w[3]);
                         }
-                        if (fix) *q = make_uint4(w[0], w[1], w[2], w[3]);
+                        odd = __hfma2(*reinterpret_cast<__nv_bfloat162 *>(&v.x), zero, odd);
+                        odd = __hfma2(*reinterpret_cast<__nv_bfloat162 *>(&v.y), zero, odd);
+                        odd = __hfma2(*reinterpret_cast<__nv_bfloat162 *>(&v.z), zero, odd);
+                        odd = __hfma2(*reinterpret_cast<__nv_bfloat162 *>(&v.w), zero, odd);
                     }
+                    const bool bad = __hisnan(__low2bfloat16(odd)) || __hisnan(__high2bfloat16(odd));
+                    if (bad)
+                        for (int c = 0; c < cend; ++c) {
+                            uint32_t *q = reinterpret_cast<uint32_t *>(row + ((c ^ r7) << 4));
+                            for (int h = 0; h < 8; ++h)
+                                if (((q[h >> 1] >> (16 * (h & 1))) & 0x7f80u) == 0x7f80u)
+                                    q[h >> 1] &= (h & 1) ? 0x0000ffffu : 0xffff0000u;
+                        }
                     if (bad) *s_bad = 1;
                     fence_proxy_async_smem();
                     mbar_arrive(dec_full(s));
@@ -536,9 +548,6 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
             const int sub = (warp - 2) >> 2;     // weight sub-tile of this warp
             uint16_t *Os = reinterpret_cast<uint16_t *>(smem);  // [NT*BN][TM] bf16; all MMAs are done
             const int m = sub * kBM + q * 32 + lane;
-            const bool bad = MULTI && *s_bad;
-            // (the output tile overwrites the stages, not the list behind them)
-            auto tok_id = [&](int k) -> int { return s_tok[k]; };
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 for (int c0 = 0; c0 < p.BN; c0 += 32) {
@@ -547,16 +556,26 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                     tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        if (c0 + j < p.BN) {
-                            float y = __uint_as_float(v[j]);
-                            if constexpr (MULTI) {
-                                if (bad) {
-                                    const int k = nt * p.BN + c0 + j, a = tok_id(k);
-                                    if (a >= 0) y += nonfinite_products(mp, a, m0 + m, t0 + k, p.out_ld, TRANS);
-                                }
-                            }
-                            Os[(nt * p.BN + c0 + j) * TM + m] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
-                        }
+                        if (c0 + j < p.BN)
+                            Os[(nt * p.BN + c0 + j) * TM + m] =
+                                __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[j])));
+                }
+            }
+            if constexpr (MULTI) {
+                if (*s_bad) {  // once more, with the products of the factors' non-finite elements
+                    qln::pdl_wait();
+                    for (int k = 0; k < NT * p.BN; ++k) {
+                        const int a = s_tok[k];
+                        if (a < 0) continue;
+                        const int nt = k / p.BN;
+                        uint32_t v;
+                        asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];"
+                                     : "=r"(v)
+                                     : "r"(tmem_d + ((uint32_t)(q * 32) << 16) + (uint32_t)((sub * NT + nt) * 256 + k - nt * p.BN)));
+                        tmem_wait_ld();
+                        const float y = __uint_as_float(v) + nonfinite_products(mp, a, m0 + m, t0 + k, p.out_ld, TRANS);
+                        Os[k * TM + m] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+                    }
                 }
             }
             asm volatile("bar.sync 1, %0;" ::"n"(C::kDecThreads) : "memory");
@@ -743,14 +762,13 @@ static cudaError_t launch_tc(const qln_nf4_weight *w, bool trans, const uint16_t
     if (view) {
         ok &= trans ? make_map_3d(&m_lw, lw, cols, r, view->count, 64, kBK)    // A [count][r][cols]
                     : make_map_3d(&m_lw, lw, r, rows, view->count, kBK, TM);   // B [count][rows][r]
-        m_lact = m_act;  // not used
     } else {
         if (!trans) ok &= make_map(&m_lw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, lw, r, rows, kBK, TM,
                                    CU_TENSOR_MAP_SWIZZLE_128B);                       // B [rows][r]
         else ok &= make_map(&m_lw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, lw, cols, r, 64, kBK,
                             CU_TENSOR_MAP_SWIZZLE_128B);                               // A [r][cols]
-        ok &= make_map(&m_lact, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, lact, r, n, kBK, BN, CU_TENSOR_MAP_SWIZZLE_128B);
     }
+    ok &= make_map(&m_lact, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, lact, r, n, kBK, BN, CU_TENSOR_MAP_SWIZZLE_128B);
     if (!ok) return cudaErrorInvalidValue;
 
     Params p;

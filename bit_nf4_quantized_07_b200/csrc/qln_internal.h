@@ -108,17 +108,15 @@ struct AdapterPlan {  // device arrays of the grouping by adapter (see adapter_p
 size_t adapter_plan_bytes(int64_t n);
 AdapterPlan adapter_plan_at(void *base, int64_t n);  // 256-byte aligned base of adapter_plan_bytes(n)
 cudaError_t launch_adapter_plan(const int32_t *ids, int64_t n, int count, const AdapterPlan &p, int *status, cudaStream_t st);
-// partial[split][t][j] = in[t] . factor_a(t)[j] over one of the K ranges of cps 64-chunks
-cudaError_t launch_adapter_down(const uint16_t *in, int64_t n, int64_t K, const uint16_t *pool, bool kmajor, int r,
-                                int count, const AdapterPlan &p, float *partial, int splits, int cps, cudaStream_t st);
-// the splits' sum as fp32, as bf16(s v) and as a bf16 pair (each may be null)
-cudaError_t launch_adapter_fold(const float *partial, int splits, int64_t n, const qln_adapter_pool *pool,
-                                const int32_t *ids, float *full, uint16_t *scaled, uint16_t *hi, uint16_t *lo, cudaStream_t st);
-cudaError_t launch_adapter_grads(const uint16_t *dY, const uint16_t *Uhi, const uint16_t *Ulo, int64_t dout,
-                                 const uint16_t *X, const uint16_t *Ghi, const uint16_t *Glo, int64_t din,
-                                 const qln_adapter_pool *pool, const AdapterPlan &p, float *dA, float *dB, cudaStream_t st);
-// split-K plan of the down products (lora_small.cu)
-void lora_down_plan(int64_t n, int64_t K, int r, int num_sms, int *splits, int *cps);
+// v[t][j] = in[t] . factor_a(t)[j] (A, or B with kmajor) as fp32, as bf16(s v) and as three bf16 planes of n * r
+// (each may be null); with aux_split also the planes of aux (fp32 [n][r])
+cudaError_t launch_adapter_down(const uint16_t *in, int64_t n, int64_t K, const qln_adapter_pool *pool, bool kmajor,
+                                const AdapterPlan &p, float *full, uint16_t *scaled, uint16_t *split, const float *aux,
+                                uint16_t *aux_split, cudaStream_t st);
+// dA and dB of every adapter; U3, G3: three bf16 planes of n * r
+cudaError_t launch_adapter_grads(const uint16_t *dY, const uint16_t *U3, int64_t dout, const uint16_t *X,
+                                 const uint16_t *G3, int64_t din, int64_t n, const qln_adapter_pool *pool,
+                                 const AdapterPlan &p, float *dA, float *dB, cudaStream_t st);
 
 // The adapters of a GEMM over tokens with adapters of their own: lact is
 // bf16(s U) [n][r] and lw the pool's factor base, `stride` elements per adapter.
