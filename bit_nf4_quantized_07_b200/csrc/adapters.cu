@@ -342,6 +342,128 @@ __global__ void __launch_bounds__(128) adapter_down_kernel(const DownArgs p) {
 }
 
 // ===========================================================================
+// Down product of a decode-sized batch (n <= 32), without a plan: every cluster
+// groups the ids by itself (one warp holds them all) and takes the x-th adapter
+// present and 16 of its columns; its 8 CTAs x 4 warps take the 64-blocks of K in
+// turn, factor rows and tokens straight from global memory into MMA fragments
+// (A operand: 16 factor rows; B operand: 8 tokens; both with the same
+// permutation of k within a block, so each load is 16 bytes).  Latency-bound: a
+// warp has all loads of two blocks in flight, and partial sums meet in shared
+// memory, first of the warps, then of the CTAs, in a fixed order.
+// ===========================================================================
+struct SmallArgs {
+    const uint16_t *in, *A;
+    int n, r, count;
+    int64_t K;
+    const int32_t *ids, *rank;
+    const float *scale;
+    float *full;       // [n][r] or null
+    uint16_t *scaled;  // [n][r]
+};
+
+template <int NT>  // n <= 8 NT
+__global__ void __launch_bounds__(128) adapter_down_small_kernel(const SmallArgs p) {
+    constexpr int LD = 8 * NT + 2;
+    __shared__ float s_part[4][16][LD], s_sum[16][LD];
+    pdl_wait();
+    pdl_trigger();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, part = blockIdx.z;
+    const int g = lane >> 2, c = lane & 3, n = p.n, r = p.r;
+    const int id = lane < n ? __ldg(p.ids + lane) : -1;
+    const bool in = (unsigned)id < (unsigned)p.count;
+    const uint32_t with = __ballot_sync(0xffffffffu, in);
+    const uint32_t same = __match_any_sync(0xffffffffu, in ? id : -1) & with;
+    const uint32_t leads = __ballot_sync(0xffffffffu, in && (same & ((1u << lane) - 1u)) == 0);
+    const int j0 = 16 * blockIdx.y;
+    if (p.full && blockIdx.x == 0 && warp == 0 && lane < n && !in)  // tokens without an adapter: two columns per CTA
+        for (int j = j0 + 2 * part; j < min(r, j0 + 2 * part + 2); ++j) p.full[lane * r + j] = 0.f;
+    if ((int)blockIdx.x >= __popc(leads)) return;  // the whole cluster
+    const int lead = __fns(leads, 0, blockIdx.x + 1);
+    const int a = __shfl_sync(0xffffffffu, id, lead);
+    const uint32_t mask = __shfl_sync(0xffffffffu, same, lead);  // its tokens
+    const int rk = adapter_rank(p.rank, a, r), cnt = __popc(mask);
+    if (j0 >= rk) {  // zero past the rank
+        if (part == 0)
+            for (int i = tid; i < 16 * cnt; i += 128) {
+                const int t = __fns(mask, 0, i / 16 + 1), j = j0 + i % 16;
+                if (j >= r) continue;
+                p.scaled[t * r + j] = 0;
+                if (p.full) p.full[t * r + j] = 0.f;
+            }
+        return;
+    }
+    const uint16_t *xr[NT];  // this lane's token of each tile, at its 16 columns of a block
+    bool xok[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        xok[nt] = 8 * nt + g < cnt;
+        xr[nt] = p.in + (xok[nt] ? (int64_t)__fns(mask, 0, 8 * nt + g + 1) * p.K : 0) + 16 * c;
+    }
+    const bool ok0 = j0 + g < r, ok1 = j0 + g + 8 < r;
+    const uint16_t *f0 = p.A + ((int64_t)a * r + (ok0 ? j0 + g : 0)) * p.K + 16 * c;
+    const uint16_t *f1 = p.A + ((int64_t)a * r + (ok1 ? j0 + g + 8 : 0)) * p.K + 16 * c;
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    float acc[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
+    const int KB = (int)(p.K / 64);
+#pragma unroll 2
+    for (int b = part * 4 + warp; b < KB; b += 32) {
+        const int64_t o = (int64_t)b * 64;
+        uint4 fa[4], xa[NT][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            fa[h] = ok0 ? __ldg(reinterpret_cast<const uint4 *>(f0 + o) + h) : z;
+            fa[2 + h] = ok1 ? __ldg(reinterpret_cast<const uint4 *>(f1 + o) + h) : z;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) xa[nt][h] = xok[nt] ? __ldg(reinterpret_cast<const uint4 *>(xr[nt] + o) + h) : z;
+        }
+#pragma unroll
+        for (int st = 0; st < 4; ++st) {  // k pairs 16c + 4 st + {0, 1} and {2, 3}
+            const uint4 u0 = fa[st >> 1], u1 = fa[2 + (st >> 1)];
+            const uint32_t av[4] = {st & 1 ? u0.z : u0.x, st & 1 ? u1.z : u1.x, st & 1 ? u0.w : u0.y, st & 1 ? u1.w : u1.y};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const uint4 x = xa[nt][st >> 1];
+                const uint32_t bv[2] = {st & 1 ? x.z : x.x, st & 1 ? x.w : x.y};
+                mma_bf16_16816(acc[nt], av, bv);
+            }
+        }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<float2 *>(&s_part[warp][g + 8 * h][8 * nt + 2 * c]) = make_float2(acc[nt][2 * h], acc[nt][2 * h + 1]);
+    __syncthreads();
+    for (int i = tid; i < 16 * cnt; i += 128) {
+        const int j = i % 16, k = i / 16;
+        s_sum[j][k] = __fadd_rn(__fadd_rn(__fadd_rn(s_part[0][j][k], s_part[1][j][k]), s_part[2][j][k]), s_part[3][j][k]);
+    }
+    __syncwarp();
+    ad_cluster_sync();
+    const float s = __ldg(p.scale + a);
+    const uint32_t base = smem_u32(&s_sum[0][0]);
+    for (int i = tid; i < 2 * cnt; i += 128) {  // two columns per CTA
+        const int j = 2 * part + (i & 1), k = i >> 1;
+        float x[kAdCluster], v = 0.f;
+#pragma unroll
+        for (int q = 0; q < kAdCluster; ++q) x[q] = ad_peer_f32(base + (uint32_t)(j * LD + k) * 4u, q);
+#pragma unroll
+        for (int q = 0; q < kAdCluster; ++q) v = __fadd_rn(v, x[q]);
+        if (j0 + j >= r) continue;
+        if (j0 + j >= rk) v = 0.f;
+        const int at = __fns(mask, 0, k + 1) * r + j0 + j;
+        if (p.full) p.full[at] = v;
+        p.scaled[at] = __bfloat16_as_ushort(__float2bfloat16_rn(__fmul_rn(s, v)));
+    }
+    __syncwarp();
+    ad_cluster_sync();  // no CTA ends while another reads its sums
+}
+
+// ===========================================================================
 // Gradients of the factors: C[m][j] = s_a sum_{t of a} P[t][m] Q[t][j], P = dY
 // and Q = U (dB_a [dout][r]), or P = X and Q = G (dA_a, stored transposed,
 // [r][din]).  A cluster of 4 CTAs owns 128 m x up to 64 j of one adapter; its
@@ -586,6 +708,19 @@ cudaError_t launch_adapter_down(const uint16_t *in, int64_t n, int64_t K, const 
     if (a.r <= 64) return QLN_AD_DOWN(8);
     return QLN_AD_DOWN(16);
 #undef QLN_AD_DOWN
+}
+
+cudaError_t launch_adapter_down_small(const uint16_t *in, int64_t n, int64_t K, const qln_adapter_pool *pool,
+                                      const int32_t *ids, float *full, uint16_t *scaled, cudaStream_t st) {
+    const SmallArgs a{in, pool->A, (int)n, pool->r, pool->count, K, ids, pool->rank, pool->scale, full, scaled};
+    const dim3 grid((unsigned)(n < pool->count ? n : pool->count), (unsigned)((pool->r + 15) / 16), kAdCluster);
+    const dim3 cl(1, 1, kAdCluster);
+    switch ((n + 7) / 8) {
+        case 1: return launch_cluster(adapter_down_small_kernel<1>, grid, cl, 0, st, a);
+        case 2: return launch_cluster(adapter_down_small_kernel<2>, grid, cl, 0, st, a);
+        case 3: return launch_cluster(adapter_down_small_kernel<3>, grid, cl, 0, st, a);
+        default: return launch_cluster(adapter_down_small_kernel<4>, grid, cl, 0, st, a);
+    }
 }
 
 template <int NTJ>

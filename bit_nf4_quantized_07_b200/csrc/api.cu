@@ -157,7 +157,7 @@ cudaError_t multi_gemm(const qln_nf4_weight *w, bool trans, const uint16_t *act,
                        const uint16_t *factors, const qln_adapter_pool *pool, const int32_t *ids, uint16_t *out,
                        int *status, cudaStream_t st, int num_sms) {
     const qln::AdapterView v{ids, pool->rank, pool->count};
-    if (qln::nf4_tc_gemm_supported(w, trans, n, pool->r))
+    if (qln::nf4_tc_gemm_multi_supported(w, trans, pool->r))
         return qln::launch_nf4_tc_gemm_multi(w, trans, act, n, lact, factors, pool->r, v, out, status, st, num_sms);
     return qln::launch_nf4_mma_gemm_multi(w, trans, act, n, lact, factors, pool->r, v, out, st);
 }
@@ -477,7 +477,14 @@ qln_status qlora_multi_fwd(const qln_nf4_weight *w, const qln_adapter_pool *pool
     const qln::AdapterPlan plan = qln::adapter_plan_at(wsb + L.plan, n);
     uint16_t *sU = reinterpret_cast<uint16_t *>(wsb + L.scaled);
     int *status = reinterpret_cast<int *>(wsb);
-    cudaError_t e = qln::launch_adapter_plan(ids, n, pool->count, plan, status, cs);
+    cudaError_t e;
+    if (qln::nf4_decode_fwd_supported(w, n, pool->r, true)) {
+        // decode-sized n: U, then the weight stream beside it (which clears the status word)
+        e = qln::launch_adapter_down_small(X, n, w->cols, pool, ids, U_out, sU, cs);
+        if (e != cudaSuccess) return QLN_ERR_CUDA;
+        return from_cuda(qln::launch_nf4_decode_fwd_multi(w, X, n, sU, pool, ids, Y, status, cs));
+    }
+    e = qln::launch_adapter_plan(ids, n, pool->count, plan, status, cs);
     if (e != cudaSuccess) return QLN_ERR_CUDA;
     e = qln::launch_adapter_down(X, n, w->cols, pool, false, plan, U_out, sU, nullptr, nullptr, nullptr, cs);
     if (e != cudaSuccess) return QLN_ERR_CUDA;

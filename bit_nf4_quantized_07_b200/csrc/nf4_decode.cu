@@ -45,6 +45,16 @@
 // Every sum is taken in an order fixed by the shape and the plan (S, nsub,
 // E), so results do not depend on timing.  No CTA waits on another cluster;
 // inside a cluster every CTA is co-scheduled by the hardware.
+// MULTI: each token has an adapter of its own from a pool.  U comes from the
+// kernel ahead (adapter_down_small_kernel), so there are no A items; this kernel
+// streams the weight while that one runs and waits for it only before the
+// folds, which is safe because that kernel lets it start only after its own
+// wait for all earlier work.  The folded tiles stay in shared memory, and the
+// warps then take (tile, adapter) pairs: one MMA pass of the tile's 16 rows of
+// that adapter's B against bf16(s U) of all tokens, stored for the adapter's own
+// tokens only (an MMA's columns do not mix, so nothing else of it is used).  The
+// B rows are requested into L2 at launch and the first of them into registers
+// before the cluster barrier.
 // Decoding layout: in each 64-wide block, lane (g, c) owns code bytes
 // 8c..8c+7 of rows g and g+8; MMA step st uses bytes 2st (k pair "2c") and
 // 2st+1 (k pair "2c+8"), and X and A are read with the same permutation of k,
@@ -64,6 +74,7 @@ constexpr int kDfTabBytes = 256 * 256;    // per code byte a 256-B row: 32 lanes
 constexpr int kDfXLines = 256;            // X lines (token, block), in the second halves of the table rows
 constexpr int kDfPartBytes = 512;         // one partial: 32 lanes x float4 (16 rows x 8 tokens)
 constexpr size_t kDfSmemMax = 232448;     // per-CTA dynamic shared memory limit of sm_100
+constexpr size_t kDfSmemMulti = kDfSmemMax - 1024;  // the MULTI kernel's: beside its static tables
 constexpr uint64_t kDfWaitNs = 2000000000ull;  // bounded waits
 
 struct DfParams {
@@ -85,6 +96,11 @@ struct DfParams {
     int *status;         // device status word
     int S, Q, nsub, nsubA, nkb_max, RS, E, JT;
     int off_ring, off_slots, off_uslots, off_sb, off_su, off_ah, off_bar;  // shared-memory layout (bytes)
+    // MULTI
+    int xs, off_x;           // X lines: distance and first line (table halves, or an area of their own)
+    const int32_t *ids, *rank;
+    int count;
+    const uint16_t *sU;      // [n][r] bf16(s U)
 };
 
 // ---- cluster and memory-model primitives -------------------------------------
@@ -115,7 +131,9 @@ __device__ __forceinline__ void df_mma_zero(float (&d)[4], const uint32_t (&a)[4
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
 }
 
-template <int NT>  // token tiles of 8: n <= 8 * NT
+constexpr int kDfPairs = 4;  // (tile, adapter) pairs of a warp whose first B fragment is loaded ahead
+
+template <int NT, bool MULTI>  // token tiles of 8: n <= 8 * NT
 __global__ void __launch_bounds__(kDfThreads, 1)
 nf4_decode_fwd_kernel(const __grid_constant__ CUtensorMap tm_codes, const DfParams p) {
     extern __shared__ __align__(1024) uint8_t dsm[];
@@ -147,6 +165,10 @@ nf4_decode_fwd_kernel(const __grid_constant__ CUtensorMap tm_codes, const DfPara
     const uint32_t bar_w = smem_u32(dsm + p.off_bar) + (uint32_t)(warp * RS * 8);
     const uint32_t slots_s = smem_u32(dsm + p.off_slots), uslots_s = smem_u32(dsm + p.off_uslots);
     const int ahs = nkbx + 1;
+    const int xs = MULTI ? p.xs : 256, x0 = MULTI ? p.off_x : 128;  // X lines
+    __shared__ int s_gid[MULTI ? 33 : 1];         // the tokens' adapters, each once; -1 for tokens without one
+    __shared__ uint32_t s_gmask[MULTI ? 33 : 1];  // their tokens
+    __shared__ int s_groups;
 
     // Before the dependency wait only shared memory and the launch's own
     // parameters are touched, nothing an earlier kernel on the stream can
@@ -233,8 +255,10 @@ nf4_decode_fwd_kernel(const __grid_constant__ CUtensorMap tm_codes, const DfPara
     // ---- 1. requests: the code boxes first (the longest latency), then X and the
     //         B rows (asynchronous copies), then the block constants, whose loads
     //         this thread waits for -- so all of them are in flight together -------------
-    pdl_wait();  // the weight, X, A, B and the workspace may be written by the previous kernel
-    pdl_trigger();
+    if (!MULTI) {
+        pdl_wait();  // the weight, X, A, B and the workspace may be written by the previous kernel
+        pdl_trigger();
+    }
     if (dq) mu = __ldg(p.dq_mean);
     if (blockIdx.x == 0 && tid == 0) *p.status = QLN_OK;
 #pragma unroll 1
@@ -244,13 +268,30 @@ nf4_decode_fwd_kernel(const __grid_constant__ CUtensorMap tm_codes, const DfPara
     for (int t = warp; t < 8 * NT; t += kDfWarps)
 #pragma unroll 1
         for (int j = lane; j < nkbx * 8; j += 32) {
-            uint8_t *dst = tab + (t * nkbx + (j >> 3)) * 256 + 128 + (((j & 7) ^ (t & 1)) << 4);
+            uint8_t *dst = tab + (t * nkbx + (j >> 3)) * xs + x0 + (((j & 7) ^ (t & 1)) << 4);
             if (t < n && j < nkb * 8)
                 cp_async16(dst, p.X + (int64_t)t * p.cols + kb0 * 64 + j * 8);
             else
                 *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
         }
-    stage_b(0);
+    if constexpr (MULTI) {
+        if (warp == 0) {  // the batch's groups
+            const int id = lane < n ? __ldg(p.ids + lane) : 0;
+            const int a = (unsigned)id < (unsigned)p.count ? id : -1;
+            const uint32_t live = n == 32 ? 0xffffffffu : (1u << n) - 1u;
+            const uint32_t same = __match_any_sync(0xffffffffu, lane < n ? a : -2) & live;
+            const bool lead = lane < n && (same & ((1u << lane) - 1u)) == 0;
+            const uint32_t leads = __ballot_sync(0xffffffffu, lead);
+            if (lead) {
+                const int at = __popc(leads & ((1u << lane) - 1u));
+                s_gid[at] = a;
+                s_gmask[at] = same;
+            }
+            if (lane == 0) s_groups = __popc(leads);
+        }
+    } else {
+        stage_b(0);
+    }
     cp_async_commit();
     stage_ah(0);
     cp_async_wait<0>();
@@ -262,7 +303,7 @@ nf4_decode_fwd_kernel(const __grid_constant__ CUtensorMap tm_codes, const DfPara
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int t = 8 * nt + g;
-        xoff[nt] = (uint32_t)((t * nkbx + sb0) * 256 + 128 + (((2 * c) ^ (t & 1)) << 4));
+        xoff[nt] = (uint32_t)((t * nkbx + sb0) * xs + x0 + (((2 * c) ^ (t & 1)) << 4));
     }
     // one 64-wide block: 4 MMA steps per token tile into tmp (A from the decode table
     // or, for A items, straight from registers)
@@ -288,9 +329,36 @@ nf4_decode_fwd_kernel(const __grid_constant__ CUtensorMap tm_codes, const DfPara
         }
     };
     int kbx = 0;  // boxes consumed by this warp
+    // MULTI: B fragment of a (tile, adapter) pair: rows row0 + g (+8), columns j0 + 2c (+8), zero past the rank
+    auto pair_frag = [&](int64_t row0, int a, int rk, int j0, uint32_t (&f)[4]) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int j = j0 + 2 * c + 8 * (q >> 1);
+            const uint16_t *src = p.B + ((int64_t)a * p.rows + row0 + g + 8 * (q & 1)) * r + j;
+            f[q] = j < rk ? __ldcg(reinterpret_cast<const uint32_t *>(src)) : 0u;
+            if (j + 1 == rk) f[q] &= 0xffffu;
+        }
+    };
+    auto pair_rank = [&](int a) -> int {
+        if (a < 0) return 0;
+        const int k = p.rank ? __ldg(p.rank + a) : r;
+        return k < 0 ? 0 : (k > r ? r : k);
+    };
 #pragma unroll 1
     for (int e = 0; e < nep; ++e) {
         const int Ee = e + 1 < nep ? E : El;
+        const int nown = Ee > rank ? (Ee - rank + S - 1) / S : 0;  // tiles this CTA folds
+        if constexpr (MULTI) {  // their rows of the adapters' B, into L2
+            const int lines = 16 * r * 2 / 128 > 0 ? 16 * r * 2 / 128 : 1, per = s_groups * lines;
+#pragma unroll 1
+            for (int i = tid; i < nown * per; i += kDfThreads) {
+                const int li = i / per, gr = (i - li * per) / lines, ln = i % lines, a = s_gid[gr];
+                if (a >= 0) {
+                    const int64_t row = (int64_t)(t0 + e * E + li * S + rank) * 16;
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(p.B + ((int64_t)a * p.rows + row) * r + ln * 64));
+                }
+            }
+        }
         // this warp's items: weight tiles ts0, ts0 + L, ...; then, in the first
         // epoch, A items w, w + 16, ... (A tile jt, block sub-range sa of nsubA)
         const int nwi = Ee > ts0 ? (Ee - ts0 + L - 1) / L : 0;
@@ -337,7 +405,7 @@ nf4_decode_fwd_kernel(const __grid_constant__ CUtensorMap tm_codes, const DfPara
                                 av[st][q] = *reinterpret_cast<const uint32_t *>(tab + off);
                             }
                         float tmp[NT][4];
-                        block_mma((uint32_t)((4 * gb + b) * 256), av, tmp, true);
+                        block_mma((uint32_t)((4 * gb + b) * xs), av, tmp, true);
                         const float ah0 = ahr[4 * gb + b], ah1 = ahr[8 * ahs + 4 * gb + b];
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
@@ -360,7 +428,7 @@ nf4_decode_fwd_kernel(const __grid_constant__ CUtensorMap tm_codes, const DfPara
                 const uint16_t *ar0 = p.A + (int64_t)(j0 < r ? j0 : 0) * p.cols + (kb0 + ab0) * 64 + 16 * c;
                 const uint16_t *ar1 = p.A + (int64_t)(j1 < r ? j1 : 0) * p.cols + (kb0 + ab0) * 64 + 16 * c;
                 const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-                const int xsh = (ab0 - sb0) * 256;  // X lines of block ab0 relative to this lane's xoff
+                const int xsh = (ab0 - sb0) * xs;  // X lines of block ab0 relative to this lane's xoff
 #pragma unroll 1
                 for (int b = 0; b < anb; ++b) {
                     const uint4 a00 = j0 < r ? df_ldg128(ar0 + b * 64) : z, a01 = j0 < r ? df_ldg128(ar0 + b * 64 + 8) : z;
@@ -368,7 +436,7 @@ nf4_decode_fwd_kernel(const __grid_constant__ CUtensorMap tm_codes, const DfPara
                     // k pairs 16c + 4 st + {0, 1} and {2, 3}
                     const uint32_t av[4][4] = {{a00.x, a10.x, a00.y, a10.y}, {a00.z, a10.z, a00.w, a10.w},
                                                {a01.x, a11.x, a01.y, a11.y}, {a01.z, a11.z, a01.w, a11.w}};
-                    block_mma((uint32_t)(xsh + b * 256), av, acc, false);
+                    block_mma((uint32_t)(xsh + b * xs), av, acc, false);
                 }
             }
             if (!waited) {
@@ -391,10 +459,32 @@ nf4_decode_fwd_kernel(const __grid_constant__ CUtensorMap tm_codes, const DfPara
         }
         if (!waited) cl_wait();
         cp_async_wait<0>();  // this thread's B-row copies of the epoch have landed
+        uint32_t pf[MULTI ? kDfPairs : 1][4];
+        if constexpr (MULTI) {
+#pragma unroll
+            for (int k = 0; k < kDfPairs; ++k) {
+                const int pr = warp + kDfWarps * k;
+                if (pr < nown * s_groups) {
+                    const int li = pr / s_groups, a = s_gid[pr - li * s_groups];
+                    if (a >= 0) pair_frag((int64_t)(t0 + e * E + li * S + rank) * 16, a, pair_rank(a), 0, pf[k]);
+                }
+            }
+        }
         cl_arrive();
+        if constexpr (MULTI) {
+            if (e == 0) {  // U is complete: bf16(s U) of the tokens, zero past the batch
+                pdl_wait();
+                pdl_trigger();
+                for (int i = tid; i < NT * 8 * r / 8; i += kDfThreads) {
+                    const int t = i / (r / 8);
+                    *reinterpret_cast<uint4 *>(sU + i * 8) =
+                        t < n ? __ldcg(reinterpret_cast<const uint4 *>(p.sU + i * 8)) : make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+        }
         cl_wait();  // every partial of the epoch has landed here
         // ---- 3. folds -----------------------------------------------------------------------
-        if (e == 0) {  // U, in the order (rank, sub-range); every CTA keeps bf16(s U)
+        if (!MULTI && e == 0) {  // U, in the order (rank, sub-range); every CTA keeps bf16(s U)
             const bool wu = p.U_out != nullptr && cl == 0 && rank == 0;
 #pragma unroll 1
             for (int pc = warp; pc < p.JT * NT; pc += kDfWarps) {
@@ -455,38 +545,94 @@ nf4_decode_fwd_kernel(const __grid_constant__ CUtensorMap tm_codes, const DfPara
                         }
                 }
             }
-#pragma unroll 1
-            for (int j0 = 0; j0 < r; j0 += 16) {
-                uint32_t a[4];
+            if constexpr (MULTI) {  // the folded tile stays in the place of its first partial
+                float4 *to = reinterpret_cast<float4 *>(dsm + p.off_slots) + (li * S * nsub * NT) * 32 + lane;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int row = g + 8 * (q & 1), j = j0 + 2 * c + 8 * (q >> 1);
-                    a[q] = j < r ? *reinterpret_cast<const uint32_t *>(sB + (li * 16 + row) * r + j) : 0u;
+                for (int nt = 0; nt < NT; ++nt) to[nt * 32] = make_float4(f[nt][0], f[nt][1], f[nt][2], f[nt][3]);
+            } else {
+#pragma unroll 1
+                for (int j0 = 0; j0 < r; j0 += 16) {
+                    uint32_t a[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int row = g + 8 * (q & 1), j = j0 + 2 * c + 8 * (q >> 1);
+                        a[q] = j < r ? *reinterpret_cast<const uint32_t *>(sB + (li * 16 + row) * r + j) : 0u;
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const int t = 8 * nt + g;
+                        uint32_t bb[2];
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const int j = j0 + 2 * c + 8 * q;
+                            bb[q] = j < r ? *reinterpret_cast<const uint32_t *>(sU + t * r + j) : 0u;
+                        }
+                        mma_bf16_16816(f[nt], a, bb);
+                    }
                 }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int t = 8 * nt + 2 * c + (q & 1);
+                        const int64_t row = row0 + g + 8 * (q >> 1);
+                        if (t < n) p.Y[(int64_t)t * p.rows + row] = __bfloat16_as_ushort(__float2bfloat16_rn(f[nt][q]));
+                    }
+            }
+        }
+        if constexpr (MULTI) {
+            __syncthreads();  // the folded tiles and bf16(s U) are in place
+            auto pair = [&](int pr, bool ahead, const uint32_t (&first)[4]) {
+                const int li = pr / s_groups, gr = pr - li * s_groups, a = s_gid[gr], rk = pair_rank(a);
+                const uint32_t mask = s_gmask[gr];
+                const int64_t row0 = (int64_t)(t0 + e * E + li * S + rank) * 16;
+                float f[NT][4];
+                const float4 *from = reinterpret_cast<const float4 *>(dsm + p.off_slots) + (li * S * nsub * NT) * 32 + lane;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const int t = 8 * nt + g;
-                    uint32_t bb[2];
+                    const float4 v = from[nt * 32];
+                    f[nt][0] = v.x, f[nt][1] = v.y, f[nt][2] = v.z, f[nt][3] = v.w;
+                }
+#pragma unroll 2
+                for (int j0 = 0; j0 < rk; j0 += 16) {
+                    uint32_t af[4];
+                    if (ahead && j0 == 0) {
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const int j = j0 + 2 * c + 8 * q;
-                        bb[q] = j < r ? *reinterpret_cast<const uint32_t *>(sU + t * r + j) : 0u;
+                        for (int q = 0; q < 4; ++q) af[q] = first[q];
+                    } else {
+                        pair_frag(row0, a, rk, j0, af);
                     }
-                    mma_bf16_16816(f[nt], a, bb);
-                }
-            }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt) {
+                        if (((mask >> (8 * nt)) & 0xffu) == 0) continue;
+                        uint32_t bb[2];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int t = 8 * nt + 2 * c + (q & 1);
-                    const int64_t row = row0 + g + 8 * (q >> 1);
-                    if (t < n) p.Y[(int64_t)t * p.rows + row] = __bfloat16_as_ushort(__float2bfloat16_rn(f[nt][q]));
+                        for (int q = 0; q < 2; ++q) {
+                            const int j = j0 + 2 * c + 8 * q;
+                            bb[q] = j < r ? *reinterpret_cast<const uint32_t *>(sU + (8 * nt + g) * r + j) : 0u;
+                        }
+                        mma_bf16_16816(f[nt], af, bb);
+                    }
                 }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int t = 8 * nt + 2 * c + (q & 1);
+                        if ((mask >> t) & 1u)
+                            p.Y[(int64_t)t * p.rows + row0 + g + 8 * (q >> 1)] = __bfloat16_as_ushort(__float2bfloat16_rn(f[nt][q]));
+                    }
+            };
+            const int npairs = nown * s_groups;
+#pragma unroll
+            for (int k = 0; k < kDfPairs; ++k)
+                if (warp + kDfWarps * k < npairs) pair(warp + kDfWarps * k, true, pf[k]);
+#pragma unroll 1
+            for (int pr = warp + kDfWarps * kDfPairs; pr < npairs; pr += kDfWarps) pair(pr, false, pf[0]);
         }
         if (e + 1 < nep) {
             __syncthreads();  // the slots, B rows and block constants of this epoch are read
-            stage_b(e + 1);
+            if (!MULTI) stage_b(e + 1);
             cp_async_commit();
             stage_ah(e + 1);
             cl_arrive();      // this CTA's slots may be refilled
@@ -498,14 +644,14 @@ nf4_decode_fwd_kernel(const __grid_constant__ CUtensorMap tm_codes, const DfPara
 // ---- host: plan and launch --------------------------------------------------------------
 struct DfLayout {
     int S, Q, nsub, nsubA, nkb_max, RS, E, JT;
-    int off_ring, off_slots, off_uslots, off_sb, off_su, off_ah, off_bar;
+    int off_ring, off_slots, off_uslots, off_sb, off_su, off_ah, off_bar, off_x;
     size_t smem;
 };
 
 static int df_a128(int64_t x) { return (int)((x + 127) & ~int64_t(127)); }
 
 // Shared-memory layout for a plan; false if it does not fit.
-static bool df_fit(DfLayout &L, int NT, int r) {
+static bool df_fit(DfLayout &L, int NT, int r, bool multi) {
     const int64_t part = (int64_t)NT * kDfPartBytes;
     const int64_t own = (L.E + L.S - 1) / L.S;  // tiles a CTA folds per epoch, at most
     int64_t off = kDfTabBytes;
@@ -516,25 +662,33 @@ static bool df_fit(DfLayout &L, int NT, int r) {
     L.off_uslots = (int)off;
     off += df_a128((int64_t)L.JT * L.S * L.nsubA * part);
     L.off_sb = (int)off;
-    off += df_a128(own * 16 * r * 2);
+    off += multi ? 0 : df_a128(own * 16 * r * 2);
     L.off_su = (int)off;
     off += df_a128((int64_t)8 * NT * r * 2);
     L.off_ah = (int)off;
     off += df_a128((int64_t)L.E * 16 * (L.nkb_max + 1) * 4);
     L.off_bar = (int)off;
     off += (int64_t)kDfWarps * L.RS * 8;
+    L.off_x = 128;  // the second halves of the table rows
+    if ((int64_t)8 * NT * L.nkb_max > kDfXLines) {
+        off = df_a128(off);
+        L.off_x = (int)off;
+        off += (int64_t)8 * NT * L.nkb_max * 128;
+    }
     L.smem = (size_t)off;
-    return off <= (int64_t)kDfSmemMax;
+    return off <= (int64_t)(multi ? kDfSmemMulti : kDfSmemMax);
 }
 
 // Plan for one cluster size S given Q clusters: sub-ranges, A sub-ranges and
 // epoch size.  Returns false if no layout fits.
-static bool df_plan_s(int64_t T, int64_t KB, int r, int NT, int S, int64_t Q, DfLayout &L) {
+// multi: no A items and no staged B rows, and the X lines may take an area of
+// their own.
+static bool df_plan_s(int64_t T, int64_t KB, int r, int NT, int S, int64_t Q, bool multi, DfLayout &L) {
     L.S = S;
     L.Q = (int)Q;
     L.nkb_max = (int)((KB + S - 1) / S);
-    L.JT = (r + 15) / 16;
-    if (S > KB || (int64_t)8 * NT * L.nkb_max > kDfXLines || Q < 1) return false;
+    L.JT = multi ? 0 : (r + 15) / 16;
+    if (S > KB || (!multi && (int64_t)8 * NT * L.nkb_max > kDfXLines) || Q < 1) return false;
     const int64_t m = (T + Q - 1) / Q;
     const int64_t nkb_min = KB / S;
     // A items (U): at most 32, ideally enough sub-ranges of one block or more for every warp to
@@ -566,14 +720,14 @@ static bool df_plan_s(int64_t T, int64_t KB, int r, int NT, int S, int64_t Q, Df
                         L.nsubA = nsa;
                         L.E = (int)E;
                         L.RS = rs;
-                        if (df_fit(L, NT, r)) return true;
+                        if (df_fit(L, NT, r, multi)) return true;
                     }
         }
         done = best_cost + 1;
     }
 }
 
-bool nf4_decode_fwd_supported(const qln_nf4_weight *w, int64_t n, int r) {
+bool nf4_decode_fwd_supported(const qln_nf4_weight *w, int64_t n, int r, bool multi) {
     if (n < 1 || n > 32 || (w->rows % 16) != 0 || (w->cols % 64) != 0 || (r % 8) != 0 || r < 8 || r > 128)
         return false;
     // the kernel's index arithmetic is 32-bit: block indices and tile counts times the grid must fit
@@ -583,12 +737,12 @@ bool nf4_decode_fwd_supported(const qln_nf4_weight *w, int64_t n, int r) {
     for (int S = 1; S <= 8; S *= 2) {
         DfLayout L;
         // one cluster per tile range is the smallest grid a device can take
-        if (df_plan_s(T, KB, r, NT, S, T < 148 / S ? T : 148 / S, L)) return true;
+        if (df_plan_s(T, KB, r, NT, S, T < 148 / S ? T : 148 / S, multi, L)) return true;
     }
     return false;
 }
 
-template <int NT>
+template <int NT, bool MULTI>
 static cudaError_t df_max_clusters(int S, int *out) {
     // per device and cluster size: co-resident clusters of one CTA per SM (0 =
     // not asked yet); host threads may launch at once, so the entries are atomics
@@ -603,7 +757,8 @@ static cudaError_t df_max_clusters(int S, int *out) {
             return cudaSuccess;
         }
     }
-    e = cudaFuncSetAttribute(nf4_decode_fwd_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDfSmemMax);
+    e = cudaFuncSetAttribute(nf4_decode_fwd_kernel<NT, MULTI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(MULTI ? kDfSmemMulti : kDfSmemMax));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t q = {};
     cudaLaunchAttribute attr[1];
@@ -613,11 +768,11 @@ static cudaError_t df_max_clusters(int S, int *out) {
     attr[0].val.clusterDim.z = 1;
     q.gridDim = dim3((unsigned)S);
     q.blockDim = dim3(kDfThreads);
-    q.dynamicSmemBytes = kDfSmemMax;
+    q.dynamicSmemBytes = MULTI ? kDfSmemMulti : kDfSmemMax;
     q.attrs = attr;
     q.numAttrs = 1;
     int nclus = 0;
-    e = cudaOccupancyMaxActiveClusters(&nclus, (const void *)nf4_decode_fwd_kernel<NT>, &q);
+    e = cudaOccupancyMaxActiveClusters(&nclus, (const void *)nf4_decode_fwd_kernel<NT, MULTI>, &q);
     if (e != cudaSuccess) return e;
     if (nclus < 1) return cudaErrorInvalidConfiguration;
     if (dev >= 0 && dev < 64) cache[dev][S].store(nclus, std::memory_order_relaxed);
@@ -625,7 +780,7 @@ static cudaError_t df_max_clusters(int S, int *out) {
     return cudaSuccess;
 }
 
-template <int NT>
+template <int NT, bool MULTI>
 static cudaError_t launch_df(DfParams p, const qln_nf4_weight *w, cudaStream_t st) {
     const int64_t KB = p.cols / 64, T = p.rows / 16;
     // cluster size: fewest weight blocks per CTA (ties: the larger S, for less X per CTA)
@@ -634,11 +789,11 @@ static cudaError_t launch_df(DfParams p, const qln_nf4_weight *w, cudaStream_t s
     for (int S = 8; S >= 1; S /= 2) {
         if (S > KB) continue;
         int nclus = 0;
-        cudaError_t e = df_max_clusters<NT>(S, &nclus);
+        cudaError_t e = df_max_clusters<NT, MULTI>(S, &nclus);
         if (e != cudaSuccess) return e;
         const int64_t Q = nclus < T ? nclus : T;
         DfLayout L;
-        if (!df_plan_s(T, KB, p.r, NT, S, Q, L)) continue;
+        if (!df_plan_s(T, KB, p.r, NT, S, Q, MULTI, L)) continue;
         const int64_t cost = ((T + Q - 1) / Q) * L.nkb_max;
         if (best_cost < 0 || cost < best_cost) {
             best_cost = cost;
@@ -667,6 +822,8 @@ static cudaError_t launch_df(DfParams p, const qln_nf4_weight *w, cudaStream_t s
     p.off_su = best.off_su;
     p.off_ah = best.off_ah;
     p.off_bar = best.off_bar;
+    p.off_x = best.off_x;
+    p.xs = best.off_x == 128 ? 256 : 128;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -681,16 +838,15 @@ static cudaError_t launch_df(DfParams p, const qln_nf4_weight *w, cudaStream_t s
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, nf4_decode_fwd_kernel<NT>, tm, p);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, nf4_decode_fwd_kernel<NT, MULTI>, tm, p);
     note_launch();
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
 
-cudaError_t launch_nf4_decode_fwd(const qln_nf4_weight *w, const uint16_t *X, int64_t n, const uint16_t *A,
-                                  const uint16_t *B, int r, float s, uint16_t *Y, uint16_t *U_out, int *status,
-                                  cudaStream_t st) {
-    DfParams p;
+static DfParams df_params(const qln_nf4_weight *w, const uint16_t *X, int64_t n, const uint16_t *B, int r, uint16_t *Y,
+                          int *status) {
+    DfParams p = {};
     p.absmax = w->absmax;
     p.qabs = w->qabs;
     p.e4m3 = w->dq_format == QLN_DQ_E4M3;
@@ -700,19 +856,42 @@ cudaError_t launch_nf4_decode_fwd(const qln_nf4_weight *w, const uint16_t *X, in
     p.cols = w->cols;
     p.X = X;
     p.n = (int)n;
-    p.A = A;
     p.B = B;
     p.r = r;
-    p.s = s;
     p.Y = Y;
-    p.U_out = U_out;
     p.status = status;
-    switch ((n + 7) / 8) {
-        case 1: return launch_df<1>(p, w, st);
-        case 2: return launch_df<2>(p, w, st);
-        case 3: return launch_df<3>(p, w, st);
-        default: return launch_df<4>(p, w, st);
+    return p;
+}
+
+template <bool MULTI>
+static cudaError_t launch_df_nt(const DfParams &p, const qln_nf4_weight *w, cudaStream_t st) {
+    switch ((p.n + 7) / 8) {
+        case 1: return launch_df<1, MULTI>(p, w, st);
+        case 2: return launch_df<2, MULTI>(p, w, st);
+        case 3: return launch_df<3, MULTI>(p, w, st);
+        default: return launch_df<4, MULTI>(p, w, st);
     }
+}
+
+cudaError_t launch_nf4_decode_fwd(const qln_nf4_weight *w, const uint16_t *X, int64_t n, const uint16_t *A,
+                                  const uint16_t *B, int r, float s, uint16_t *Y, uint16_t *U_out, int *status,
+                                  cudaStream_t st) {
+    DfParams p = df_params(w, X, n, B, r, Y, status);
+    p.A = A;
+    p.s = s;
+    p.U_out = U_out;
+    return launch_df_nt<false>(p, w, st);
+}
+
+cudaError_t launch_nf4_decode_fwd_multi(const qln_nf4_weight *w, const uint16_t *X, int64_t n, const uint16_t *sU,
+                                        const qln_adapter_pool *pool, const int32_t *ids, uint16_t *Y, int *status,
+                                        cudaStream_t st) {
+    DfParams p = df_params(w, X, n, pool->B, pool->r, Y, status);
+    p.ids = ids;
+    p.rank = pool->rank;
+    p.count = pool->count;
+    p.sU = sU;
+    return launch_df_nt<true>(p, w, st);
 }
 
 }  // namespace qln

@@ -732,6 +732,10 @@ bool nf4_tc_gemm_supported(const qln_nf4_weight *w, bool trans, int64_t n, int r
            tc::encode_fn() != nullptr;
 }
 
+bool nf4_tc_gemm_multi_supported(const qln_nf4_weight *w, bool trans, int r) {
+    return nf4_tc_gemm_supported(w, trans, 64, r);
+}
+
 int64_t nf4_tc_gemm_ctas(const qln_nf4_weight *w, bool trans, int64_t n, int r, int num_sms) {
     if (!nf4_tc_gemm_supported(w, trans, n, r)) return 0;
     const int64_t M = trans ? w->cols : w->rows;

@@ -113,6 +113,9 @@ cudaError_t launch_adapter_plan(const int32_t *ids, int64_t n, int count, const 
 cudaError_t launch_adapter_down(const uint16_t *in, int64_t n, int64_t K, const qln_adapter_pool *pool, bool kmajor,
                                 const AdapterPlan &p, float *full, uint16_t *scaled, uint16_t *split, const float *aux,
                                 uint16_t *aux_split, cudaStream_t st);
+// the same for n <= 32 without a plan, A only (full may be null; columns past a rank are zero in both)
+cudaError_t launch_adapter_down_small(const uint16_t *in, int64_t n, int64_t K, const qln_adapter_pool *pool,
+                                      const int32_t *ids, float *full, uint16_t *scaled, cudaStream_t st);
 // dA and dB of every adapter; U3, G3: three bf16 planes of n * r
 cudaError_t launch_adapter_grads(const uint16_t *dY, const uint16_t *U3, int64_t dout, const uint16_t *X,
                                  const uint16_t *G3, int64_t din, int64_t n, const qln_adapter_pool *pool,
@@ -146,7 +149,11 @@ constexpr int kWsHeaderBytes = 256;
 // nf4_decode.cu: the whole forward for decode-sized n (<= 32) in one launch of
 // thread-block clusters: U = X A^T, Y = bf16(X W'^T + bf16(s U) B^T),
 // U_out = bf16(U) (if not null).  Needs no workspace beyond the status word.
-bool nf4_decode_fwd_supported(const qln_nf4_weight *w, int64_t n, int r);
+bool nf4_decode_fwd_supported(const qln_nf4_weight *w, int64_t n, int r, bool multi = false);
+// with a pool of adapters: sU [n][r] of launch_adapter_down_small, which is launched just before
+cudaError_t launch_nf4_decode_fwd_multi(const qln_nf4_weight *w, const uint16_t *X, int64_t n, const uint16_t *sU,
+                                        const qln_adapter_pool *pool, const int32_t *ids, uint16_t *Y, int *status,
+                                        cudaStream_t st);
 cudaError_t launch_nf4_decode_fwd(const qln_nf4_weight *w, const uint16_t *X, int64_t n, const uint16_t *A,
                                   const uint16_t *B, int r, float s, uint16_t *Y, uint16_t *U_out, int *status,
                                   cudaStream_t st);
@@ -159,5 +166,6 @@ cudaError_t launch_nf4_tc_gemm_multi(const qln_nf4_weight *w, bool trans, const 
                                      const uint16_t *lact, const uint16_t *lw, int r, const AdapterView &v,
                                      uint16_t *out, int *status, cudaStream_t st, int num_sms);
 bool nf4_tc_gemm_supported(const qln_nf4_weight *w, bool trans, int64_t n, int r);
+bool nf4_tc_gemm_multi_supported(const qln_nf4_weight *w, bool trans, int r);  // any n
 
 }  // namespace qln
