@@ -10,6 +10,7 @@ Function names follow the C entry points: ``nf4_quantize``,
 ``qlora_linear_bwd``, plus ``workspace_bytes``, ``codebook``, ``version``.
 """
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -140,16 +141,25 @@ def _need_cuda(*ts):
             raise ValueError("tensors must be contiguous CUDA tensors")
 
 
-def _need_current(device, *ts):
-    """Contiguous CUDA tensors of `device`, which is the current one: the call
-    goes to the current device's current stream."""
+def _need_current(index, *ts):
+    """Contiguous CUDA tensors of device `index`, which is the current one: the
+    call goes to the current device's current stream."""
+    for t in ts:
+        if t is not None and (t.get_device() != index or not t.is_contiguous()):
+            raise ValueError(f"tensors must be contiguous CUDA tensors of one device (cuda:{index})")
+    if index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{index}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _cuda_index(device):
     if device.type != "cuda":
         raise ValueError("tensors must be contiguous CUDA tensors")
-    for t in ts:
-        if t is not None and (t.device != device or not t.is_contiguous()):
-            raise ValueError("tensors must be contiguous CUDA tensors of one device")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    return device.index
+
+
+def _raw_stream(index) -> int:
+    """The current stream of a device, as the C ABI takes it."""
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def version() -> int:
@@ -443,65 +453,84 @@ class AdapterPool:
                 raise ValueError(f"{name} holds {t.numel()} elements, needs {count}")
         self.A, self.B, self.scale, self.rank = A, B, scale, rank
         self.count, self.r, self.din, self.dout, self.device = count, r, A.shape[2], B.shape[1], A.device
+        self.index = A.get_device()  # -1: not a CUDA tensor; the calls refuse it
         self.c = CAdapterPool(A.data_ptr(), B.data_ptr(), scale.data_ptr(), None if rank is None else rank.data_ptr(),
                               count, r)
 
 
 def _check_multi(w: NF4Weight, pool: AdapterPool, X, ids, others):
     """Shapes, types and device of a call with a pool (the library works on raw
-    pointers); others: (name, tensor or None, dtype, shape)."""
-    n = X.shape[0]
-    if (w.rows, w.cols) != (pool.dout, pool.din):
+    pointers); others: (name, tensor or None, dtype, shape).  Returns the device's index."""
+    if w.rows != pool.dout or w.cols != pool.din:
         raise ValueError(f"the weight is {w.rows} x {w.cols}, the pool's adapters {pool.dout} x {pool.din}")
+    n = X.shape[0]
+    index = pool.index
     for name, t, dt, shape in (("X", X, torch.bfloat16, (n, w.cols)), ("ids", ids, torch.int32, (n,)), *others):
-        if t is not None and (t.dtype != dt or t.shape != shape):
+        if t is None:
+            continue
+        if t.dtype != dt or t.shape != shape:
             raise ValueError(f"{name} must be {dt} {shape}, got {t.dtype} {tuple(t.shape)}")
-    _need_current(pool.device, X, ids, w.codes, w.absmax, w.qabs, w.dq_scale, w.dq_mean, *(o[1] for o in others))
+        if t.get_device() != index or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor on the pool's device")
+    if index < 0:
+        raise ValueError("tensors must be contiguous CUDA tensors")
+    _need_current(index, w.codes, w.absmax, w.qabs, w.dq_scale, w.dq_mean)
+    return index
 
 
-def _multi_workspace(op, w, n, r, ws, device):
+@functools.lru_cache(maxsize=1024)
+def _multi_workspace_bytes(op, rows, cols, n, r):
+    return workspace_bytes(op, rows, cols, n, r)
+
+
+def _multi_workspace(op, w, n, r, ws, pool):
     """The call's scratch (it keeps no state, so it need not be zeroed)."""
     if ws is None:
-        return torch.empty(workspace_bytes(op, w.rows, w.cols, n, r), dtype=torch.uint8, device=device)
-    _need_current(device, ws)
+        return w.codes.new_empty(_multi_workspace_bytes(op, w.rows, w.cols, n, r))  # uint8
+    _need_current(pool.index, ws)
     return ws
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def qlora_multi_fwd(w: NF4Weight, pool: AdapterPool, X, ids, Y=None, U_out=None, ws=None, want_u: bool = False):
     """Y_t = X_t W'^T + s_a (X_t A_a^T) B_a^T with a = ids[t] (none if outside the
     pool).  Returns (Y [n][dout] bf16, U [n][r] fp32 or None)."""
     n = X.shape[0]
-    _check_multi(w, pool, X, ids, (("Y", Y, torch.bfloat16, (n, w.rows)), ("U_out", U_out, torch.float32, (n, pool.r))))
-    dev = pool.device
+    index = _check_multi(w, pool, X, ids, (("Y", Y, torch.bfloat16, (n, w.rows)),
+                                           ("U_out", U_out, torch.float32, (n, pool.r))))
     if Y is None:
-        Y = torch.empty(n, w.rows, dtype=torch.bfloat16, device=dev)
+        Y = X.new_empty(n, w.rows)
     if U_out is None and want_u:
-        U_out = torch.empty(n, pool.r, dtype=torch.float32, device=dev)
-    ws = _multi_workspace(OP_MULTI_FWD, w, n, pool.r, ws, dev)
-    cw = w.c_struct()
-    _check("qlora_multi_fwd", lib().qlora_multi_fwd(ctypes.byref(cw), ctypes.byref(pool.c), _p(X), n, _p(ids), _p(Y),
-                                                    _p(U_out), _p(ws), ws.numel(), _stream()))
+        U_out = pool.scale.new_empty(n, pool.r)
+    ws = _multi_workspace(OP_MULTI_FWD, w, n, pool.r, ws, pool)
+    _check("qlora_multi_fwd", lib().qlora_multi_fwd(ctypes.byref(w.c_struct()), ctypes.byref(pool.c), X.data_ptr(), n,
+                                                    ids.data_ptr(), Y.data_ptr(), _ptr(U_out), ws.data_ptr(),
+                                                    ws.numel(), _raw_stream(index)))
     return Y, U_out
 
 
 def qlora_multi_bwd(w: NF4Weight, pool: AdapterPool, X, ids, dY, U=None, dX=None, dA=None, dB=None, ws=None):
     """Returns (dX [n][din] bf16, dA [count][r][din] fp32, dB [count][dout][r] fp32)."""
     n = X.shape[0]
-    _check_multi(w, pool, X, ids, (("dY", dY, torch.bfloat16, (n, w.rows)), ("U", U, torch.float32, (n, pool.r)),
-                                   ("dX", dX, torch.bfloat16, (n, w.cols)),
-                                   ("dA", dA, torch.float32, (pool.count, pool.r, w.cols)),
-                                   ("dB", dB, torch.float32, (pool.count, w.rows, pool.r))))
-    dev = pool.device
+    index = _check_multi(w, pool, X, ids, (("dY", dY, torch.bfloat16, (n, w.rows)),
+                                           ("U", U, torch.float32, (n, pool.r)),
+                                           ("dX", dX, torch.bfloat16, (n, w.cols)),
+                                           ("dA", dA, torch.float32, (pool.count, pool.r, w.cols)),
+                                           ("dB", dB, torch.float32, (pool.count, w.rows, pool.r))))
     if dX is None:
-        dX = torch.empty(n, w.cols, dtype=torch.bfloat16, device=dev)
+        dX = X.new_empty(n, w.cols)
     if dA is None:
-        dA = torch.empty(pool.count, pool.r, w.cols, dtype=torch.float32, device=dev)
+        dA = pool.scale.new_empty(pool.count, pool.r, w.cols)
     if dB is None:
-        dB = torch.empty(pool.count, w.rows, pool.r, dtype=torch.float32, device=dev)
-    ws = _multi_workspace(OP_MULTI_BWD, w, n, pool.r, ws, dev)
-    cw = w.c_struct()
-    _check("qlora_multi_bwd", lib().qlora_multi_bwd(ctypes.byref(cw), ctypes.byref(pool.c), _p(X), n, _p(ids), _p(dY),
-                                                    _p(U), _p(dX), _p(dA), _p(dB), _p(ws), ws.numel(), _stream()))
+        dB = pool.scale.new_empty(pool.count, w.rows, pool.r)
+    ws = _multi_workspace(OP_MULTI_BWD, w, n, pool.r, ws, pool)
+    _check("qlora_multi_bwd", lib().qlora_multi_bwd(ctypes.byref(w.c_struct()), ctypes.byref(pool.c), X.data_ptr(), n,
+                                                    ids.data_ptr(), dY.data_ptr(), _ptr(U), dX.data_ptr(),
+                                                    dA.data_ptr(), dB.data_ptr(), ws.data_ptr(), ws.numel(),
+                                                    _raw_stream(index)))
     return dX, dA, dB
 
 
@@ -616,9 +645,11 @@ def _multi_step(fn, tensors, cls, step, lr, betas, eps, weight_decay, flags):
         raise ValueError(f"tensors must be {cls.__name__}, got {type(tensors).__name__}")
     if step.dtype != torch.int64 or step.numel() < 1:
         raise ValueError("step must be an int64 tensor holding the step number")
-    _need_current(tensors.device, step)
+    index = _cuda_index(tensors.device)
+    _need_current(index, step)
     cfg = CAdamWConfig(lr, betas[0], betas[1], eps, weight_decay)
-    _check(fn, getattr(lib(), fn)(tensors.array, tensors.count, ctypes.byref(cfg), _p(step), flags, _stream()))
+    _check(fn, getattr(lib(), fn)(tensors.array, tensors.count, ctypes.byref(cfg), step.data_ptr(), flags,
+                                  _raw_stream(index)))
 
 
 def adamw_multi_step(tensors: AdamWTensors, step: torch.Tensor, lr: float, betas=(0.9, 0.999), eps: float = 1e-8,

@@ -131,6 +131,12 @@ __device__ __forceinline__ void df_mma_zero(float (&d)[4], const uint32_t (&a)[4
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
 }
 
+// MULTI: the book enters the tensor cores as bf16(gamma c), and ahat / gamma
+// scales the partial.  gamma = 1 rounds the 16 entries with a relative error of
+// 1.06e-3 in norm; of the 2,000,000 evenly spaced gammas in [1, 2) this one does
+// best, with 0.63e-3 (largest single error 1.93e-3 instead of 3.1e-3).
+constexpr float kDfGamma = 1.437006f;
+
 constexpr int kDfPairs = 4;  // (tile, adapter) pairs of a warp whose first B fragment is loaded ahead
 
 template <int NT, bool MULTI>  // token tiles of 8: n <= 8 * NT
@@ -180,10 +186,11 @@ nf4_decode_fwd_kernel(const __grid_constant__ CUtensorMap tm_codes, const DfPara
         tc::tma_prefetch_map(&tm_codes);
     }
     {   // table: warp w writes the rows e = 16 k + w, so c[e & 15] = c[w] is a constant
-        const float clo = nf4_value(warp);
+        const float gamma = MULTI ? kDfGamma : 1.f;
+        const float clo = nf4_value(warp) * gamma;
 #pragma unroll
         for (int k = 0; k < 16; ++k)  // k is a compile-time index: c[k] is a literal
-            *reinterpret_cast<uint32_t *>(tab + (16 * k + warp) * 256 + lane * 4) = pack_bf16x2(nf4_value(k), clo);
+            *reinterpret_cast<uint32_t *>(tab + (16 * k + warp) * 256 + lane * 4) = pack_bf16x2(nf4_value(k) * gamma, clo);
     }
     __syncwarp();
 
@@ -248,7 +255,8 @@ nf4_decode_fwd_kernel(const __grid_constant__ CUtensorMap tm_codes, const DfPara
 #pragma unroll
             for (int u = 0; u < 4; ++u)
                 if (b0 + u < nkb)
-                    sAh[tr * ahs + b0 + u] = dq ? dq_restore(raw[u], sc[u], mu, p.e4m3) : __uint_as_float(raw[u]);
+                    sAh[tr * ahs + b0 + u] =
+                        (dq ? dq_restore(raw[u], sc[u], mu, p.e4m3) : __uint_as_float(raw[u])) * (MULTI ? 1.f / kDfGamma : 1.f);
         }
     };
 
@@ -794,7 +802,10 @@ static cudaError_t launch_df(DfParams p, const qln_nf4_weight *w, cudaStream_t s
         const int64_t Q = nclus < T ? nclus : T;
         DfLayout L;
         if (!df_plan_s(T, KB, p.r, NT, S, Q, MULTI, L)) continue;
-        const int64_t cost = ((T + Q - 1) / Q) * L.nkb_max;
+        // blocks per CTA; with MULTI also 50 for every epoch after the first, about what its barriers and refills
+        // cost (4096 x 11008, n = 12: one epoch on clusters of 8 takes XX us, four on clusters of 4 take 67 us)
+        const int64_t m = (T + Q - 1) / Q;
+        const int64_t cost = m * L.nkb_max + (MULTI ? 50 * ((m + L.E - 1) / L.E - 1) : 0);
         if (best_cost < 0 || cost < best_cost) {
             best_cost = cost;
             best = L;

@@ -25,17 +25,23 @@
 //   the adapter term is extra K steps whose A_op (B or A, zero-padded to 64)
 //     and B_op (s*U or s*G) both arrive by TMA.
 // MULTI: each token has an adapter of its own from a pool.  The adapter term
-// takes ceil(rank / 64) k-steps per adapter present among the tile's tokens, in
-// the order of their first tokens (warp 1 lists them while the pipeline
-// fills).  Such a step's A_op is the adapter's factor (3-D map, so rows past
-// the factor read as zero), its B_op s*U or s*G, both by TMA; the decoders then
-// write zeros over the other adapters' tokens.  All MMAs keep one shape: only
+// goes by chunks of 16 columns: the first 16 of every adapter present among the
+// tile's tokens (warp 1 lists them while the pipeline fills), then the next 16
+// of those with a larger rank, and so on; a k-step takes the next four chunks,
+// whichever adapters they belong to.  A chunk's A_op is 16 columns of the
+// adapter's factor by TMA in 32-byte rows (dX: 16 rows of it, as in a weight
+// step; 3-D maps, so what lies past the factor reads as zero).  Its B_op is
+// written by the decoders: s*U or s*G of the adapter's own tokens, copied
+// asynchronously one k-step ahead, zero for the others; a stage's zeros stay
+// where they are from step to step.  (One warp per scheduler has nothing to
+// hide its instructions behind: writing every row in every step took 1.5 us per
+// k-step.)  All MMAs keep one shape: only
 // then do they run in the order of their issue.  A zero times an infinity would
 // still be a NaN, so the decoders also replace what is not finite in the
 // factor's tile by zero, and the epilogue adds those products to their own
-// tokens one by one (a path that finite factors never take).  An adapter step
-// costs as much as a weight step at most; a prefill tile of packed sequences
-// has one or two.
+// tokens one by one (a path that finite factors never take).  A k-step of
+// chunks costs about as much as a weight step; a prefill tile of packed
+// sequences has one or two.
 // A MULTI kernel reads its activations and weights before the kernel ahead of
 // it on the stream has completed, and waits for that one only before the
 // adapter steps.  This is safe because the call's first kernel waits for all
@@ -77,11 +83,11 @@ struct Cfg {
     static constexpr uint32_t kNumBars = 4 * kStages + 2;
     static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;  // tmem base, abort flag, epilogue go
     static constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;  // + alignment slack
-    // MULTI: the tile's adapters (16-bit entries: the adapter of each token, then the list: adapter, first and last
-    // token; and the list's place of every adapter of the pool)
+    // MULTI: the tile's list of adapters (one word each), the adapter of each token, and the list's place of every
+    // adapter of the pool (16 bits each)
     static constexpr int kTok = NT * kMaxBN;
     static constexpr uint32_t kOffList = kOffMisc + 16;
-    static constexpr uint32_t kListBytes = (4 * kTok + QLN_MAX_ADAPTERS) * 2 + 16;
+    static constexpr uint32_t kListBytes = kTok * 6 + QLN_MAX_ADAPTERS * 2 + 16;
     static constexpr uint32_t kSmemBytesMulti = kSmemBytes + kListBytes;
     static_assert(kSmemBytesMulti <= 232448, "shared memory of one CTA");
 };
@@ -127,7 +133,7 @@ template <bool TRANS, int MT, int NT, bool MULTI>
 __global__ void __launch_bounds__(Cfg<MT, NT>::kThreads, 1)
 nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_act,
                    const __grid_constant__ CUtensorMap tm_lw, const __grid_constant__ CUtensorMap tm_lact,
-                   const Params p, const MultiParams mp) {
+                   const Params p, const __grid_constant__ MultiParams mp) {
     using C = Cfg<MT, NT>;
     constexpr int S = C::kStages;
     constexpr int TM = kBM * MT;  // rows of the CTA tile
@@ -150,17 +156,61 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
     const int64_t m0 = (int64_t)blockIdx.y * TM;
     const int nsteps = p.KT + (MULTI ? 0 : p.RT);
     // MULTI: the tile's adapters
-    int16_t *s_tok = reinterpret_cast<int16_t *>(smem + C::kOffList);
-    int16_t *s_who = s_tok + C::kTok, *s_first = s_who + C::kTok, *s_last = s_first + C::kTok, *s_place = s_last + C::kTok;
+    uint32_t *s_list = reinterpret_cast<uint32_t *>(smem + C::kOffList);  // adapter | rank << 12 | sub-tiles << 24
+    int16_t *s_tok = reinterpret_cast<int16_t *>(s_list + C::kTok);
+    int16_t *s_place = s_tok + C::kTok;
     volatile int *s_count = reinterpret_cast<volatile int *>(s_place + QLN_MAX_ADAPTERS);  // adapters of the tile
     volatile int *s_bad = s_count + 1;                                                     // a factor is not finite
-    auto rank_of = [&](int a) -> int {
-        if (!mp.rank) return mp.r;
-        const int k = __ldg(mp.rank + a);
-        return k < 0 ? 0 : (k > mp.r ? mp.r : k);
+    // The chunks in their order, for a whole warp.  A batch covers E = 2^k entries of the list (all of them, up to 32)
+    // and 32 / E columns-of-16; lane i holds its i-th chunk: entry | (first column / 16) << 26.
+    struct Chunks {
+        int na, E, e0, j0, cnt, pos;
+        uint32_t d, mask;  // mask: which of the batch's E x 32 / E places are chunks
     };
-    // whether the list's adapter e may have tokens in sub-tile nt (first and last token of the tile)
-    auto in_sub = [&](int e, int nt) -> bool { return s_first[e] < (nt + 1) * p.BN && s_last[e] >= nt * p.BN; };
+    auto refill = [&](Chunks &k) -> bool {  // to the next batch with a chunk; false past the last
+        for (;;) {
+            k.e0 += k.E;
+            if (k.e0 >= k.na) {
+                k.e0 = 0;
+                k.j0 += 16 * (32 / k.E);
+                if (k.j0 >= mp.r) return false;
+            }
+            const int e = k.e0 + (lane & (k.E - 1)), j = k.j0 + 16 * (lane / k.E);
+            const uint32_t own = (e < k.na ? s_list[e] : 0u) | (uint32_t)(j >> 4) << 26;
+            const uint32_t mask = __ballot_sync(0xffffffffu, (int)((own >> 12) & 0xffu) > j && j < mp.r);
+            if (!mask) continue;
+            int src = 0;  // the lane of the mask's lane-th bit
+#pragma unroll
+            for (int h = 16; h > 0; h >>= 1)
+                if (__popc(mask & ((1u << (src + h)) - 1u)) <= lane) src += h;
+            k.d = __shfl_sync(0xffffffffu, own, src);
+            k.mask = mask;
+            k.cnt = __popc(mask);
+            k.pos = 0;
+            return true;
+        }
+    };
+    auto begin = [&](Chunks &k) -> bool {
+        k.na = *s_count;
+        k.E = k.na <= 1 ? 1 : (k.na > 16 ? 32 : 1 << (32 - __clz(k.na - 1)));
+        k.e0 = -k.E;
+        k.j0 = 0;
+        return k.na > 0 && refill(k);
+    };
+    auto take = [&](Chunks &k, uint32_t (&ent)[4]) -> bool {  // the next step's chunks (0: none); whether more follow
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t d = __shfl_sync(0xffffffffu, k.d, (k.pos + q) & 31);
+            ent[q] = k.pos + q < k.cnt ? d : 0u;
+        }
+        k.pos += 4;
+        return k.pos < k.cnt || refill(k);
+    };
+    auto ent_who = [](uint32_t d) { return (int)(d & 0xfffu); };
+    auto ent_col = [](uint32_t d) { return (int)(d >> 26) * 16; };
+    auto ent_left = [](uint32_t d) { return (int)((d >> 12) & 0xffu) - (int)(d >> 26) * 16; };  // columns to the rank's end
+    constexpr uint32_t kAChunk = 4096u * MT;               // TM rows of 32 bytes
+    const uint32_t bchunk = (uint32_t)(NT * p.BN) * 32u;   // the tile's tokens, 32 bytes each
     if (MULTI)
         for (int i = threadIdx.x; i < QLN_MAX_ADAPTERS; i += C::kThreads) s_place[i] = -1;
 
@@ -181,7 +231,7 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
         tma_prefetch_map(&tm_codes);
         tma_prefetch_map(&tm_act);
         tma_prefetch_map(&tm_lw);
-        tma_prefetch_map(&tm_lact);
+        if (!MULTI) tma_prefetch_map(&tm_lact);
     }
     if (warp == 1) {
         tmem_alloc(smem_addr(tmem_slot), C::kTmemCols);
@@ -205,10 +255,10 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
+        int issued = 0;
         if (lane == 0) {
             const uint32_t bsub = (uint32_t)p.BN * kBK * 2;  // one token sub-tile
             const uint32_t bbytes = NT * bsub;
-            int issued = 0;
             for (int kt = 0; kt < nsteps; ++kt) {
                 const int s = kt % S;
                 const uint32_t ph = (uint32_t)(kt / S) & 1u;
@@ -248,39 +298,49 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                 }
                 issued = kt + 1;
             }
-            if constexpr (MULTI) {
+        }
+        if constexpr (MULTI) {
+            bool ok = true;
+            if (lane == 0) {
                 qln::pdl_wait();  // s U or s G is there
                 qln::pdl_trigger();
-                if (issued == nsteps && !mbar_wait_bounded(list_full, 0, abort_flag, kWaitLimitNs)) {
-                    give_up();
-                } else if (issued == nsteps) {
-                    const int na = *s_count;
-                    for (int e = 0; e < na && !*abort_flag; ++e) {
-                        const int a = s_who[e], rk = rank_of(a);
-                        for (int j = 0; j < rk; j += kBK) {
-                            const int s = issued % S;
-                            if (!mbar_wait_bounded(empty(s), ((uint32_t)(issued / S) & 1u) ^ 1u, abort_flag, kWaitLimitNs)) {
-                                give_up();
-                                break;
-                            }
-                            const uint32_t sA = sbase + C::kOffA + s * C::kABytes;
-                            mbar_arrive_expect_tx(tma_full(s), C::kABytes + bbytes);
+                ok = issued == nsteps && mbar_wait_bounded(list_full, 0, abort_flag, kWaitLimitNs);
+                if (!ok) give_up();
+            }
+            issued = __shfl_sync(0xffffffffu, issued, 0);
+            __syncwarp();  // the list, which lane 0 has waited for
+            Chunks k;
+            bool more = __shfl_sync(0xffffffffu, ok, 0) && begin(k);
+            while (more) {
+                const int s = issued % S;
+                const uint32_t sA = sbase + C::kOffA + s * C::kABytes;
+                uint32_t ent[4];
+                more = take(k, ent);
+                if (lane == 0) {
+                    ok = mbar_wait_bounded(empty(s), ((uint32_t)(issued / S) & 1u) ^ 1u, abort_flag, kWaitLimitNs);
+                    if (ok) {
+                        mbar_arrive_expect_tx(tma_full(s), (1 + (ent[1] != 0) + (ent[2] != 0) + (ent[3] != 0)) * kAChunk);
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                tma_load_2d(sbase + C::kOffB + s * C::kBBytes + nt * bsub, &tm_lact, j,
-                                            (int32_t)(t0 + nt * p.BN), tma_full(s));
+                        for (int q = 0; q < 4; ++q) {
+                            if (!ent[q]) break;
+                            const int who = ent_who(ent[q]), col = ent_col(ent[q]);
                             if (!TRANS) {
-                                tma_load_3d(sA, &tm_lw, j, (int32_t)m0, a, tma_full(s));
+                                tma_load_3d(sA + q * kAChunk, &tm_lw, col, (int32_t)m0, who, tma_full(s));
                             } else {
 #pragma unroll
                                 for (int d = 0; d < 2 * MT; ++d)
-                                    tma_load_3d(sA + 8192 * d, &tm_lw, (int32_t)m0 + 64 * d, j, a, tma_full(s));
+                                    tma_load_3d(sA + 8192 * d + 2048 * q, &tm_lw, (int32_t)m0 + 64 * d, col, who, tma_full(s));
                             }
-                            ++issued;
                         }
+                    } else {
+                        give_up();
                     }
                 }
+                if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+                ++issued;
             }
+        }
+        if (lane == 0) {
             // Drain: every issued copy has landed before the CTA may exit.
             for (int kt = (issued > S ? issued - S : 0); kt < issued; ++kt) {
                 const int s = kt % S;
@@ -306,17 +366,20 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
 #pragma unroll
             for (int i = 0; i < (C::kTok + 31) / 32; ++i) {
                 const uint32_t same = __match_any_sync(0xffffffffu, id[i]);
+                const uint32_t first = __ballot_sync(0xffffffffu, 32 * i + lane < p.BN);  // tokens of sub-tile 0
                 const bool lead = id[i] >= 0 && (same & ((1u << lane) - 1u)) == 0;
                 int at = lead ? s_place[id[i]] : 0;
                 const uint32_t fresh = __ballot_sync(0xffffffffu, lead && at < 0);
                 if (lead) {
+                    const uint32_t subs = ((same & first) ? 1u << 24 : 0u) | ((same & ~first) ? 1u << 25 : 0u);
                     if (at < 0) {
                         at = na + __popc(fresh & ((1u << lane) - 1u));
                         s_place[id[i]] = (int16_t)at;
-                        s_who[at] = (int16_t)id[i];
-                        s_first[at] = (int16_t)(32 * i + lane);
+                        const int k = mp.rank ? __ldg(mp.rank + id[i]) : mp.r;
+                        s_list[at] = (uint32_t)id[i] | (uint32_t)min(max(k, 0), mp.r) << 12 | subs;
+                    } else {
+                        s_list[at] |= subs;
                     }
-                    s_last[at] = (int16_t)(32 * i + 31 - __clz(same));
                 }
                 na += __popc(fresh);
                 __syncwarp();
@@ -358,39 +421,47 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                 }
                 tc_commit(empty(s));
             }
-            if constexpr (MULTI) {
-                const int na = *s_count;
-                int kt = nsteps;
-                for (int e = 0; e < na && !*abort_flag; ++e) {
-                    const int rk = rank_of(s_who[e]);
-                    for (int j = 0; j < rk; j += kBK, ++kt) {
-                        const int s = kt % S;
-                        const uint32_t ph = (uint32_t)(kt / S) & 1u;
-                        if (!mbar_wait_bounded(tma_full(s), ph, abort_flag, kWaitLimitNs) ||
-                            !mbar_wait_bounded(dec_full(s), ph, abort_flag, kWaitLimitNs)) {
-                            give_up();
-                            break;
-                        }
+        }
+        if constexpr (MULTI) {
+            const uint32_t idesc = idesc_bf16_f32(kBM, p.BN, TRANS, false);
+            __syncwarp();
+            Chunks k;
+            bool more = begin(k);
+            for (int kt = nsteps; more; ++kt) {
+                const int s = kt % S;
+                const uint32_t ph = (uint32_t)(kt / S) & 1u;
+                uint32_t ent[4];
+                more = take(k, ent);
+                bool ok = true;
+                if (lane == 0) {
+                    ok = mbar_wait_bounded(tma_full(s), ph, abort_flag, kWaitLimitNs) &&
+                         mbar_wait_bounded(dec_full(s), ph, abort_flag, kWaitLimitNs);
+                    if (ok) {
                         tc_fence_after();
                         const uint32_t sA = sbase + C::kOffA + s * C::kABytes;
                         const uint32_t sB = sbase + C::kOffB + s * C::kBBytes;
-                        const int ks = rk - j < kBK ? (rk - j + 15) / 16 : kBK / 16;
-                        for (int nt = 0; nt < NT; ++nt) {
-                            if (!in_sub(e, nt)) continue;
-                            for (int sub = 0; sub < MT; ++sub) {
-                                const uint32_t aS = sA + sub * 16384;
-                                for (int k = 0; k < ks; ++k) {
-                                    const uint64_t adesc = TRANS ? smem_desc_sw128(aS + k * 2048, 8192, 1024)
-                                                                 : smem_desc_sw128(aS + k * 32, 16, 1024);
-                                    const uint64_t bdesc = smem_desc_sw128(sB + nt * p.BN * 128 + k * 32, 16, 1024);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                if (!((ent[q] >> (24 + nt)) & 1u)) continue;  // none of its tokens, or no chunk
+                                const uint64_t bdesc = smem_desc_sw32(sB + q * bchunk + nt * p.BN * 32);
+#pragma unroll
+                                for (int sub = 0; sub < MT; ++sub) {
+                                    const uint64_t adesc = TRANS ? smem_desc_sw128(sA + sub * 16384 + q * 2048, 8192, 1024)
+                                                                 : smem_desc_sw32(sA + q * kAChunk + sub * 4096);
                                     tc_mma_ss(tmem_d + (sub * NT + nt) * 256, adesc, bdesc, idesc, 1u);
                                 }
                             }
-                        }
                         tc_commit(empty(s));
+                    } else {
+                        give_up();
                     }
                 }
+                if (!__shfl_sync(0xffffffffu, ok, 0)) break;
             }
+        }
+        if (lane == 0) {
             tc_commit(accum_full);
         }
     } else {
@@ -475,64 +546,177 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
         }
         if constexpr (MULTI) {
             if (!*abort_flag && !mbar_wait_bounded(list_full, 0, abort_flag, kWaitLimitNs)) give_up();
-            const int na = *abort_flag ? 0 : *s_count;
-            int kt = nsteps;
-            for (int e = 0; e < na && !*abort_flag; ++e) {
-                const int a = s_who[e], rk = rank_of(a);
-                for (int j = 0; j < rk; j += kBK, ++kt) {
-                    const int s = kt % S;
-                    const uint32_t ph = (uint32_t)(kt / S) & 1u;
-                    const int left = rk - j < kBK ? rk - j : kBK, cks = 2 * ((left + 15) / 16);  // 8-wide chunks
-                    const uint32_t sB = sbase + C::kOffB + s * C::kBBytes;
-                    if (!mbar_wait_bounded(tma_full(s), ph, abort_flag, kWaitLimitNs)) {
-                        give_up();
-                        break;
-                    }
-                    for (int nt = 0; nt < NT; ++nt) {
-                        if (!in_sub(e, nt)) continue;
-                        for (int row = dt; row < p.BN; row += C::kDecThreads) {
-                            if (s_tok[nt * p.BN + row] == a) continue;
-                            const uint32_t at = sB + (nt * p.BN + row) * 128;
-                            for (int c = 0; c < cks; ++c)
-                                st_shared_v4(at + ((c ^ (row & 7)) << 4), make_uint4(0u, 0u, 0u, 0u));
-                        }
-                    }
-                    // The factor's tile: zero past the rank, and where it is not finite.  One thread per
-                    // 128-byte row: 64 columns j of one m, or 64 m of one row j.
-                    uint8_t *row = smem + C::kOffA + s * C::kABytes + (TRANS ? dcol * 8192 + drow * 128 : dt * 128);
-                    const int r7 = (TRANS ? drow : dt) & 7;
-                    const int cend = TRANS ? (drow < 8 * cks ? 8 : 0) : cks;  // chunks that the MMA reads
-                    const int keep = TRANS ? (drow < left ? 64 : 0) : left;   // columns before the rank's end
-                    __nv_bfloat162 odd = __float2bfloat162_rn(0.f);           // NaN once an element is not finite
-                    const __nv_bfloat162 zero = odd;
-                    for (int c = 0; c < cend; ++c) {
-                        uint4 *q = reinterpret_cast<uint4 *>(row + ((c ^ r7) << 4));
-                        uint4 v = *q;
-                        if (8 * c + 8 > keep) {  // (partly) past the rank
-                            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            qln::pdl_wait();  // s U or s G is there
+            constexpr int kRows = (C::kTok + C::kDecThreads - 1) / C::kDecThreads;
+            // This thread's tokens: their adapters' places in the list (-1: none); the next chunk of the batch that is
+            // theirs, as its place and its number (kNone: none left); and the chunks of each stage that hold values of
+            // them (4 bits a stage).
+            constexpr int kNone = 1 << 20;
+            int place[kRows], at[kRows], num[kRows];
+            uint32_t held[kRows];
 #pragma unroll
-                            for (int h = 0; h < 8; ++h)
-                                if (8 * c + h >= keep) w[h >> 1] &= (h & 1) ? 0x0000ffffu : 0xffff0000u;
-                            *q = v = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
-                        odd = __hfma2(*reinterpret_cast<__nv_bfloat162 *>(&v.x), zero, odd);
-                        odd = __hfma2(*reinterpret_cast<__nv_bfloat162 *>(&v.y), zero, odd);
-                        odd = __hfma2(*reinterpret_cast<__nv_bfloat162 *>(&v.z), zero, odd);
-                        odd = __hfma2(*reinterpret_cast<__nv_bfloat162 *>(&v.w), zero, odd);
-                    }
-                    const bool bad = __hisnan(__low2bfloat16(odd)) || __hisnan(__high2bfloat16(odd));
-                    if (bad)
-                        for (int c = 0; c < cend; ++c) {
-                            uint32_t *q = reinterpret_cast<uint32_t *>(row + ((c ^ r7) << 4));
-                            for (int h = 0; h < 8; ++h)
-                                if (((q[h >> 1] >> (16 * (h & 1))) & 0x7f80u) == 0x7f80u)
-                                    q[h >> 1] &= (h & 1) ? 0x0000ffffu : 0xffff0000u;
-                        }
-                    if (bad) *s_bad = 1;
-                    fence_proxy_async_smem();
-                    mbar_arrive(dec_full(s));
-                }
+            for (int i = 0; i < kRows; ++i) {
+                const int row = dt + i * C::kDecThreads, tok = row < NT * p.BN ? s_tok[row] : -1;
+                place[i] = tok >= 0 ? s_place[tok] : -1;
+                held[i] = 0u;
             }
+            Chunks k{};
+            auto seek = [&](int i, int to) {  // token i's chunk at the batch's place `to`, or none
+                at[i] = to;
+                num[i] = to < 32 && ((k.mask >> to) & 1u) ? __popc(k.mask & ((1u << to) - 1u)) : kNone;
+            };
+            // B_op of the next step, kt: s U or s G of each chunk's own tokens (asynchronous copies), zeros for the
+            // others.  A stage is cleared on its first use; later, only what its last step held is.
+            auto put = [&](int kt) {
+                const int s = kt % S, step = k.pos >> 2;
+                const uint32_t sB = sbase + C::kOffB + s * C::kBBytes;
+                if (k.pos == 0) {
+#pragma unroll
+                    for (int i = 0; i < kRows; ++i) {
+                        const int to = place[i] - k.e0;
+                        seek(i, place[i] >= 0 && to >= 0 && to < k.E ? to : 32);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) {
+                    if (i * C::kDecThreads >= NT * p.BN) break;  // no rows left
+                    const int row = dt + i * C::kDecThreads;
+                    uint32_t old = (held[i] >> (4 * s)) & 15u, now = 0u;
+                    if (kt - nsteps < S) old = row < NT * p.BN ? 15u : 0u;
+                    const uint32_t to = sB + row * 32 + (((row >> 2) & 1) << 4);  // 32-byte swizzle: halves at `to` and to ^ 16
+                    while ((num[i] >> 2) == step) {
+                        const int q = num[i] & 3, j = k.j0 + 16 * (at[i] / k.E);
+                        const uint16_t *src = mp.lact + (t0 + row) * mp.r + j;
+                        const int half2 = j + 8 < mp.r ? 16 : 0;  // r = 8: the second half is zero
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to + q * bchunk), "l"(src) : "memory");
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"((to + q * bchunk) ^ 16u),
+                                     "l"(half2 ? src + 8 : src), "r"(half2)
+                                     : "memory");
+                        now |= 1u << q;
+                        seek(i, at[i] + k.E);
+                    }
+                    held[i] = (held[i] & ~(15u << (4 * s))) | now << (4 * s);
+                    for (old &= ~now; old; old &= old - 1) {
+                        const uint32_t d = to + (__ffs(old) - 1) * bchunk;
+                        st_shared_v4(d, make_uint4(0u, 0u, 0u, 0u));
+                        st_shared_v4(d ^ 16u, make_uint4(0u, 0u, 0u, 0u));
+                    }
+                }
+                qln::cp_async_commit();
+            };
+            // the stage's MMAs of S steps before have read it
+            auto free_stage = [&](int kt) -> bool {
+                const bool ok = mbar_wait_bounded(empty(kt % S), ((uint32_t)(kt / S) & 1u) ^ 1u, abort_flag, kWaitLimitNs);
+                if (!ok) give_up();
+                return __all_sync(0xffffffffu, ok);
+            };
+            // One step is written while the copies of the one before are on their way.  ent: its chunks, nq their count;
+            // with equal ranks only the count is needed (nothing lies past a rank but the map's own zeros).
+            uint32_t ent[4] = {0u, 0u, 0u, 0u}, nxt[4] = {0u, 0u, 0u, 0u};
+            int nq = 0, nxq = 0;
+            bool more = __all_sync(0xffffffffu, !*abort_flag) && begin(k);
+            auto advance = [&](int kt) -> bool {  // puts step kt and moves on
+                if (!free_stage(kt)) return false;
+                put(kt);
+                nxq = min(4, k.cnt - k.pos);
+                if (mp.rank) {
+                    more = take(k, nxt);
+                } else {
+                    k.pos += 4;
+                    more = k.pos < k.cnt || refill(k);
+                }
+                return true;
+            };
+            bool live = more && advance(nsteps);
+            for (int kt = nsteps; live; ++kt) {
+                const int s = kt % S;
+                nq = nxq;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) ent[q] = nxt[q];
+                live = more;
+                if (more) {
+                    if (!advance(kt + 1)) break;
+                    qln::cp_async_wait<1>();
+                } else {
+                    qln::cp_async_wait<0>();
+                }
+                const bool ok = mbar_wait_bounded(tma_full(s), (uint32_t)(kt / S) & 1u, abort_flag, kWaitLimitNs);
+                if (!ok) give_up();
+                if (!__all_sync(0xffffffffu, ok)) break;
+                // The factors' chunks: zero past the rank, and where they are not finite.  A thread takes the
+                // columns of one m in all chunks (32 bytes each), or one row j of a chunk (128 bytes of m).
+                uint8_t *sA = smem + C::kOffA + s * C::kABytes;
+                const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+                // x 0 added up: NaN exactly if an element is not finite
+                __nv_bfloat162 o0 = zero, o1 = zero, o2 = zero, o3 = zero;
+                auto look = [&](const uint4 &v) {
+                    o0 = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v.x), zero, o0);
+                    o1 = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v.y), zero, o1);
+                    o2 = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v.z), zero, o2);
+                    o3 = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v.w), zero, o3);
+                };
+                auto odd = [&]() { return __hadd2(__hadd2(o0, o1), __hadd2(o2, o3)); };
+                auto is_odd = [](const __nv_bfloat162 &v) { return __hisnan(__low2bfloat16(v)) || __hisnan(__high2bfloat16(v)); };
+                auto clear = [](uint4 *q, int n) {  // the non-finite of n vectors of 8
+                    uint32_t *w = reinterpret_cast<uint32_t *>(q);
+                    for (int h = 0; h < 8 * n; ++h)
+                        if (((w[h >> 1] >> (16 * (h & 1))) & 0x7f80u) == 0x7f80u)
+                            w[h >> 1] &= (h & 1) ? 0x0000ffffu : 0xffff0000u;
+                };
+                bool bad = false;
+                if (!TRANS) {
+                    // row dt: its two 16-byte halves change places where bit 7 of the address is set
+                    uint4 *row = reinterpret_cast<uint4 *>(sA + dt * 32);
+                    if (mp.rank) {
+                        const int swap = (dt >> 2) & 1;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            for (int h = ent[q] ? ent_left(ent[q]) : 16; h < 16; ++h)
+                                reinterpret_cast<uint16_t *>(row + q * (kAChunk / 16) + ((h >> 3) ^ swap))[h & 7] = 0;
+                    }
+                    uint4 v[4][2];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            v[q][h] = q < nq ? row[q * (kAChunk / 16) + h] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        look(v[q][0]);
+                        look(v[q][1]);
+                    }
+                    if (is_odd(odd())) {
+                        bad = true;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (q < nq) clear(row + q * (kAChunk / 16), 2);
+                    }
+                } else {
+                    const int q = drow >> 4;
+                    uint4 *row = reinterpret_cast<uint4 *>(sA + dcol * 8192 + drow * 128);
+                    const uint32_t e = q == 0 ? ent[0] : q == 1 ? ent[1] : q == 2 ? ent[2] : ent[3];
+                    if (q < nq) {
+                        if (mp.rank && (drow & 15) >= ent_left(e)) {  // past the rank
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) row[c ^ r8] = make_uint4(0u, 0u, 0u, 0u);
+                        } else {
+                            uint4 v[8];
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) v[c] = row[c ^ r8];
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) look(v[c]);
+                            if (is_odd(odd())) {
+                                bad = true;
+                                clear(row, 8);
+                            }
+                        }
+                    }
+                }
+                if (bad) *s_bad = 1;
+                fence_proxy_async_smem();
+                mbar_arrive(dec_full(s));
+            }
+            qln::cp_async_wait<0>();
         }
 
         // ------------------------------------------------------------ epilogue
@@ -624,7 +808,7 @@ static EncodeTiledFn encode_fn() {
 
 // 3D map over a row-major bf16 [outer][mid][inner] array, boxes of one outer index.
 static bool make_map_3d(CUtensorMap *m, const void *base, uint64_t inner, uint64_t mid, uint64_t outer,
-                        uint32_t box_inner, uint32_t box_mid) {
+                        uint32_t box_inner, uint32_t box_mid, CUtensorMapSwizzle sw) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[3] = {inner, mid, outer};
@@ -632,7 +816,7 @@ static bool make_map_3d(CUtensorMap *m, const void *base, uint64_t inner, uint64
     cuuint32_t box[3] = {box_inner, box_mid, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -764,15 +948,16 @@ static cudaError_t launch_tc(const qln_nf4_weight *w, bool trans, const uint16_t
                         CU_TENSOR_MAP_SWIZZLE_NONE);
     ok &= make_map(&m_act, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, act, K, n, kBK, BN, CU_TENSOR_MAP_SWIZZLE_128B);
     if (view) {
-        ok &= trans ? make_map_3d(&m_lw, lw, cols, r, view->count, 64, kBK)    // A [count][r][cols]
-                    : make_map_3d(&m_lw, lw, r, rows, view->count, kBK, TM);   // B [count][rows][r]
+        ok &= trans ? make_map_3d(&m_lw, lw, cols, r, view->count, 64, 16, CU_TENSOR_MAP_SWIZZLE_128B)   // A [count][r][cols]
+                    : make_map_3d(&m_lw, lw, r, rows, view->count, 16, TM, CU_TENSOR_MAP_SWIZZLE_32B);   // B [count][rows][r]
+        m_lact = m_act;  // not used
     } else {
         if (!trans) ok &= make_map(&m_lw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, lw, r, rows, kBK, TM,
                                    CU_TENSOR_MAP_SWIZZLE_128B);                       // B [rows][r]
         else ok &= make_map(&m_lw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, lw, cols, r, 64, kBK,
                             CU_TENSOR_MAP_SWIZZLE_128B);                               // A [r][cols]
+        ok &= make_map(&m_lact, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, lact, r, n, kBK, BN, CU_TENSOR_MAP_SWIZZLE_128B);
     }
-    ok &= make_map(&m_lact, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, lact, r, n, kBK, BN, CU_TENSOR_MAP_SWIZZLE_128B);
     if (!ok) return cudaErrorInvalidValue;
 
     Params p;
