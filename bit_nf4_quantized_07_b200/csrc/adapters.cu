@@ -1,14 +1,12 @@
 // Products around a pool of adapters, where every token has an adapter of its
-// own (or none): the plan that groups tokens by adapter, the products down to
-// the rank, and the gradients of the factors.
+// own (or none): the plan that groups tokens by adapter and the products down
+// to the rank.  (The gradients of the factors: adapter_grads.cu.)
 //
 // Method: "LoRA 与 QLoRA" section LoRA (y = W0 x + s B(A x), A x formed first;
 // only A and B are trained); deck "3 QLoRA Finetuning" card 1 (gradients flow
 // through the dequantized weight, only the adapters receive updates).  For
 // token t with adapter a = ids[t]:
-//   U_t = X_t A_a^T                    (forward)
-//   G_t = dY_t B_a                     (backward)
-//   dA_a = s_a sum_{t: ids[t] = a} G_t^T X_t,  dB_a = s_a sum dY_t^T U_t
+//   U_t = X_t A_a^T (forward),  G_t = dY_t B_a (backward)
 // Tokens are never multiplied with another adapter's factors, not even by a
 // zero: an infinity or NaN in one adapter or token stays with it.
 #include "qln_common.cuh"
@@ -463,178 +461,6 @@ __global__ void __launch_bounds__(128) adapter_down_small_kernel(const SmallArgs
     ad_cluster_sync();  // no CTA ends while another reads its sums
 }
 
-// ===========================================================================
-// Gradients of the factors: C[m][j] = s_a sum_{t of a} P[t][m] Q[t][j], P = dY
-// and Q = U (dB_a [dout][r]), or P = X and Q = G (dA_a, stored transposed,
-// [r][din]).  A cluster of 4 CTAs owns 128 m x up to 64 j of one adapter; its
-// CTAs take the adapter's 32-token steps in turn (gathered rows, a cp.async
-// ring), so that one long sequence does not leave a single CTA at work, and add
-// their tiles in the order of the CTAs through shared memory.  HBM-bound: every
-// activation is read once (per 64 columns), nothing is written but the result,
-// and the order of every sum is fixed.  Q enters as three bf16 parts, three
-// MMAs each, so that the fp32 result keeps fp32 accuracy; running sums move into
-// fp32 registers every 512 tokens.  Adapters without tokens get zeros, and so
-// do columns past an adapter's rank.
-// ===========================================================================
-constexpr int kAgBM = 128, kAgBK = 32, kAgPad = 136, kAgStages = 4, kAgFlush = 16, kAgCluster = 4;
-
-struct GradArgs {
-    const uint16_t *P[2], *Q[2];  // 0: dB, 1: dA; Q: three planes of n * r
-    int64_t M[2];
-    float *C[2];
-    const int32_t *order, *start, *rank;
-    const float *scale;
-    int64_t plane;
-    int r, tilesB, jchunks;
-};
-
-template <int NTJ>  // 8 NTJ columns
-__global__ void __launch_bounds__(128) adapter_grad_kernel(const GradArgs p) {
-    extern __shared__ __align__(16) uint16_t sk[];
-    constexpr int QW = NTJ * 8, QLD = QW + 8;
-    constexpr int STAGE = kAgBK * (kAgPad + 3 * QLD);
-    constexpr int PLD = QW + 4;  // padded row (fp32) of the partial tile
-    static_assert(kAgBM * PLD * 4 <= kAgStages * STAGE * 2, "the partial tile fits into the ring");
-    __shared__ int s_row[2][kAgBK];  // tokens of a step, read one step ahead
-    pdl_wait();
-    pdl_trigger();
-    const int mtile = blockIdx.y / p.jchunks, j0 = (int)(blockIdx.y % p.jchunks) * QW;
-    const int which = mtile < p.tilesB ? 0 : 1;
-    const int a = blockIdx.z, part = blockIdx.x, r = p.r;
-    const int64_t M = p.M[which], m0 = (int64_t)(mtile - (which ? p.tilesB : 0)) * kAgBM;
-    const uint16_t *P = p.P[which], *Q = p.Q[which];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = lane >> 2, c = lane & 3, mat = lane >> 3;
-    const int p0 = __ldg(p.start + a), cnt = __ldg(p.start + a + 1) - p0;
-    const int allsteps = (cnt + kAgBK - 1) / kAgBK;
-    const int steps = allsteps > part ? (allsteps - part + kAgCluster - 1) / kAgCluster : 0;
-    auto token = [&](int step) -> int {  // thread < 32: its token of this CTA's step, or -1
-        const int q = (step * kAgCluster + part) * kAgBK + tid;
-        return step < steps && q < cnt ? __ldg(p.order + p0 + q) : -1;
-    };
-
-    float acc[2][NTJ][4], sum[2][NTJ][4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < NTJ; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][j][e] = sum[i][j][e] = 0.f;
-
-    auto load = [&](int buf, const int *rows) {
-        uint16_t *Ps = sk + buf * STAGE, *Qs = Ps + kAgBK * kAgPad;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {  // P: 32 rows x 16 chunks
-            const int idx = tid + 128 * i, row = idx >> 4, ck = idx & 15, t = rows[row];
-            const int64_t col = m0 + 8 * ck;
-            const bool ok = t >= 0 && col < M;
-            cp_async16_zfill(Ps + row * kAgPad + 8 * ck, ok ? P + (int64_t)t * M + col : P, ok ? 16 : 0);
-        }
-#pragma unroll
-        for (int k = 0; k < 3; ++k)  // Q: three parts of 32 rows x NTJ chunks
-            for (int idx = tid; idx < kAgBK * NTJ; idx += 128) {
-                const int row = idx / NTJ, ck = idx % NTJ, t = rows[row];
-                const bool ok = t >= 0 && j0 + 8 * ck < r;
-                cp_async16_zfill(Qs + (k * kAgBK + row) * QLD + 8 * ck,
-                                 ok ? Q + k * p.plane + (int64_t)t * r + j0 + 8 * ck : Q, ok ? 16 : 0);
-            }
-    };
-    auto flush = [&]() {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < NTJ; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    sum[i][j][e] = __fadd_rn(sum[i][j][e], acc[i][j][e]);
-                    acc[i][j][e] = 0.f;
-                }
-    };
-    if (tid < kAgBK) s_row[0][tid] = token(0);
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kAgStages - 1; ++i) {
-        const int next = tid < kAgBK ? token(i + 1) : 0;
-        load(i, s_row[i & 1]);
-        cp_async_commit();
-        if (tid < kAgBK) s_row[(i + 1) & 1][tid] = next;
-        __syncthreads();
-    }
-    for (int it = 0; it < steps; ++it) {
-        const int nx = it + kAgStages - 1;  // the step loaded now; its tokens are in s_row[nx & 1]
-        const int next = tid < kAgBK ? token(nx + 1) : 0;
-        if (nx < steps) load(nx % kAgStages, s_row[nx & 1]);
-        cp_async_commit();
-        cp_async_wait<kAgStages - 1>();
-        if (tid < kAgBK) s_row[(nx + 1) & 1][tid] = next;
-        __syncthreads();
-        const uint16_t *Ps = sk + (it % kAgStages) * STAGE, *Qb = Ps + kAgBK * kAgPad;
-#pragma unroll
-        for (int kk = 0; kk < kAgBK; kk += 16) {
-            uint32_t af[2][4];
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
-                ldmatrix_x4_trans(af[mt][0], af[mt][1], af[mt][2], af[mt][3],
-                                  Ps + (kk + (mat >> 1) * 8 + (lane & 7)) * kAgPad + warp * 32 + mt * 16 + (mat & 1) * 8);
-#pragma unroll
-            for (int h = 0; h < 3; ++h) {
-                const uint16_t *Qs = Qb + (h * kAgBK + kk + (mat & 1) * 8 + (lane & 7)) * QLD;
-#pragma unroll
-                for (int np = 0; np < NTJ / 2; ++np) {
-                    uint32_t r0, r1, r2, r3;
-                    ldmatrix_x4_trans(r0, r1, r2, r3, Qs + np * 16 + (mat >> 1) * 8);
-                    const uint32_t b0[2] = {r0, r1}, b1[2] = {r2, r3};
-#pragma unroll
-                    for (int mt = 0; mt < 2; ++mt) {
-                        mma_bf16_16816(acc[mt][2 * np], af[mt], b0);
-                        mma_bf16_16816(acc[mt][2 * np + 1], af[mt], b1);
-                    }
-                }
-                if (NTJ & 1) {
-                    uint32_t r0, r1;
-                    ldmatrix_x2_trans(r0, r1, Qs + (NTJ - 1) * 8);
-                    const uint32_t b0[2] = {r0, r1};
-#pragma unroll
-                    for (int mt = 0; mt < 2; ++mt) mma_bf16_16816(acc[mt][NTJ - 1], af[mt], b0);
-                }
-            }
-        }
-        if (it % kAgFlush == kAgFlush - 1) flush();
-        __syncthreads();
-    }
-    cp_async_wait<0>();
-    flush();
-    float *part_s = reinterpret_cast<float *>(sk);  // this CTA's partial tile [128][PLD]
-    __syncthreads();
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < NTJ; ++nt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                *reinterpret_cast<float2 *>(part_s + (warp * 32 + mt * 16 + g + 8 * h) * PLD + nt * 8 + 2 * c) =
-                    make_float2(sum[mt][nt][2 * h], sum[mt][nt][2 * h + 1]);
-    ad_cluster_sync();
-    const int rk = cnt > 0 ? adapter_rank(p.rank, a, r) : 0;
-    const float s = __ldg(p.scale + a);
-    const uint32_t base = smem_u32(part_s);
-    float *C = p.C[which] + (int64_t)a * M * r;
-    const int jw = min(QW, r - j0);
-    for (int i = tid; i < 32 * jw; i += 128) {  // 32 m x jw columns per CTA
-        const int m = 32 * part + (which ? i & 31 : i / jw), j = which ? i >> 5 : i % jw;
-        if (m0 + m >= M) continue;
-        float x[kAgCluster], v = 0.f;
-#pragma unroll
-        for (int q = 0; q < kAgCluster; ++q) x[q] = ad_peer_f32(base + (uint32_t)(m * PLD + j) * 4u, q);
-#pragma unroll
-        for (int q = 0; q < kAgCluster; ++q) v = __fadd_rn(v, x[q]);
-        v = j0 + j < rk ? __fmul_rn(s, v) : 0.f;
-        C[which ? (int64_t)(j0 + j) * M + m0 + m : (m0 + m) * r + j0 + j] = v;
-    }
-    __syncwarp();
-    ad_cluster_sync();  // no CTA ends while another reads its tile
-}
-
 // ---- host --------------------------------------------------------------------
 static size_t r256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -721,34 +547,6 @@ cudaError_t launch_adapter_down_small(const uint16_t *in, int64_t n, int64_t K, 
         case 3: return launch_cluster(adapter_down_small_kernel<3>, grid, cl, 0, st, a);
         default: return launch_cluster(adapter_down_small_kernel<4>, grid, cl, 0, st, a);
     }
-}
-
-template <int NTJ>
-static cudaError_t launch_ad_grad(GradArgs &a, int count, cudaStream_t st) {
-    constexpr size_t smem = (size_t)kAgStages * kAgBK * (kAgPad + 3 * (NTJ * 8 + 8)) * sizeof(uint16_t);
-    const unsigned tilesA = (unsigned)((a.M[1] + kAgBM - 1) / kAgBM);
-    a.jchunks = (a.r + 8 * NTJ - 1) / (8 * NTJ);
-    return launch_cluster(adapter_grad_kernel<NTJ>, dim3(kAgCluster, (a.tilesB + tilesA) * a.jchunks, (unsigned)count),
-                          dim3(kAgCluster), smem, st, a);
-}
-
-cudaError_t launch_adapter_grads(const uint16_t *dY, const uint16_t *U3, int64_t dout, const uint16_t *X,
-                                 const uint16_t *G3, int64_t din, int64_t n, const qln_adapter_pool *pool,
-                                 const AdapterPlan &p, float *dA, float *dB, cudaStream_t st) {
-    GradArgs a;
-    a.P[0] = dY, a.P[1] = X;
-    a.Q[0] = U3, a.Q[1] = G3;
-    a.M[0] = dout, a.M[1] = din;
-    a.C[0] = dB, a.C[1] = dA;
-    a.order = p.order, a.start = p.start, a.rank = pool->rank;
-    a.scale = pool->scale;
-    a.plane = n * pool->r;
-    a.r = pool->r;
-    a.tilesB = (int)((dout + kAgBM - 1) / kAgBM);
-    if (a.r <= 8) return launch_ad_grad<1>(a, pool->count, st);
-    if (a.r <= 16) return launch_ad_grad<2>(a, pool->count, st);
-    if (a.r <= 32) return launch_ad_grad<4>(a, pool->count, st);
-    return launch_ad_grad<8>(a, pool->count, st);
 }
 
 }  // namespace qln

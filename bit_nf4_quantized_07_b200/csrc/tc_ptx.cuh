@@ -140,6 +140,15 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&v)
           "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(taddr));
 }
+// The same with 16 columns.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // ---- descriptors -------------------------------------------------------------
@@ -162,6 +171,20 @@ __device__ __forceinline__ uint64_t smem_desc_sw32(uint32_t saddr) {
     d |= (uint64_t)(256u >> 4) << 32;
     d |= (uint64_t)1u << 46;  // descriptor version for sm_100
     d |= (uint64_t)6u << 61;  // SWIZZLE_32B
+    return d;
+}
+
+// MN-major operand in rows (one K each) of ROWB = 32, 64 or 128 swizzled bytes:
+// 8-row groups are 8 ROWB bytes apart, blocks of ROWB / 2 elements `lbo_bytes`.
+template <int ROWB>
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr, uint32_t lbo_bytes) {
+    static_assert(ROWB == 32 || ROWB == 64 || ROWB == 128, "swizzle widths");
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((lbo_bytes >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)((8u * ROWB) >> 4) << 32;
+    d |= (uint64_t)1u << 46;  // descriptor version for sm_100
+    d |= (uint64_t)(ROWB == 128 ? 2u : ROWB == 64 ? 4u : 6u) << 61;
     return d;
 }
 
