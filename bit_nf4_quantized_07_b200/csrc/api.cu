@@ -519,7 +519,7 @@ qln_status qlora_multi_bwd(const qln_nf4_weight *w, const qln_adapter_pool *pool
     }
     e = qln::launch_adapter_down(dY, n, w->rows, pool, true, plan, nullptr, sG, G3, U, U ? U3 : nullptr, cs);
     if (e != cudaSuccess) return QLN_ERR_CUDA;
-    e = qln::launch_adapter_grads(dY, U3, w->rows, X, G3, w->cols, n, pool, plan, dA, dB, status, cs);
+    e = qln::launch_adapter_grads(dY, U3, w->rows, X, G3, w->cols, n, pool, plan, dA, dB, status, cs, sms);
     if (e != cudaSuccess) return QLN_ERR_CUDA;
     return from_cuda(multi_gemm(w, true, dY, n, sG, pool->A, pool, ids, dX, status, cs, sms));
 }

@@ -119,7 +119,8 @@ cudaError_t launch_adapter_down_small(const uint16_t *in, int64_t n, int64_t K, 
 // adapter_grads.cu: dA and dB of every adapter; U3, G3: three bf16 planes of n * r
 cudaError_t launch_adapter_grads(const uint16_t *dY, const uint16_t *U3, int64_t dout, const uint16_t *X,
                                  const uint16_t *G3, int64_t din, int64_t n, const qln_adapter_pool *pool,
-                                 const AdapterPlan &p, float *dA, float *dB, int *status, cudaStream_t st);
+                                 const AdapterPlan &p, float *dA, float *dB, int *status, cudaStream_t st,
+                                 int num_sms);
 
 // The adapters of a GEMM over tokens with adapters of their own: lact is
 // bf16(s U) [n][r] and lw the pool's factor base, `stride` elements per adapter.
