@@ -10,13 +10,18 @@
 //   p = p - (lr / (1 - b1^t)) m / (sqrt(v / (1 - b2^t)) + eps)
 //
 // 8-bit states.  Blocks of 256 consecutive elements of a tensor share one fp32
-// scale b = max|x| / 448 and hold E4M3 codes of x / b, the group format that
+// scale b = max|x| / 448 and hold E4M3 codes of x (448 / max|x|), the group format that
 // the double quantization uses for the block constants.  The first moment is
 // held as x = m, the second as x = sqrt(v): its square spans 2^36 within a
 // block instead of 2^18.  A nonzero sqrt(v) is never rounded to zero (it takes
 // the smallest code): a zero denominator under a nonzero m would turn the step
 // into lr m / eps.  The update itself runs in fp32 on the restored states, and
-// uses the new v before it is rounded.
+// uses the new v before it is rounded.  Per element its 18 bytes leave about
+// 100 issue slots at the HBM rate: with correctly rounded quotients, roots and
+// separate products the step needed all of them (448 tensors, 40 M elements:
+// 226 us, 49 % of the HBM rate); it uses fused products, one division per block
+// for the codes, and the hardware's approximate root and quotient (2 and 4
+// units of 2^-24, next to a code's 2^-4).
 //
 // Both kernels are HBM-bound.  The tensors' pointers travel as a kernel
 // parameter (up to 32 KB), so nothing is copied or allocated and a captured
@@ -30,6 +35,7 @@ namespace qln {
 
 constexpr int kMtChunk = 2048;   // elements per CTA step: 256 threads x 8
 constexpr int kMtThreads = 256;
+constexpr int kMtCtas = 4;       // per SM, one wave
 constexpr int kBlock8 = QLN_ADAMW8_BLOCK;
 constexpr float kE4m3Max = 448.f;
 
@@ -78,15 +84,13 @@ __device__ __forceinline__ MtStep mt_step(const MtArgs &a) {
     return s;
 }
 
-// One element in fp32; returns sqrt(v).
-__device__ __forceinline__ float mt_elem(float &p, float g, float &m, float &v, const MtArgs &a, const MtStep &s) {
+// One element in fp32.
+__device__ __forceinline__ void mt_elem(float &p, float g, float &m, float &v, const MtArgs &a, const MtStep &s) {
     m = __fadd_rn(__fmul_rn(a.b1, m), __fmul_rn(1.0f - a.b1, g));
     v = __fadd_rn(__fmul_rn(a.b2, v), __fmul_rn(1.0f - a.b2, __fmul_rn(g, g)));
     p = __fmul_rn(p, 1.0f - a.lr * a.wd);
-    const float rv = __fsqrt_rn(v);
-    const float denom = __fadd_rn(__fmul_rn(rv, s.inv_sqrt_bc2), a.eps);
+    const float denom = __fadd_rn(__fmul_rn(__fsqrt_rn(v), s.inv_sqrt_bc2), a.eps);
     p = __fsub_rn(p, __fmul_rn(s.step_size, __fdiv_rn(m, denom)));
-    return rv;
 }
 
 // The CTA's share of the chunks and the tensor its first chunk lies in.
@@ -109,7 +113,7 @@ __device__ __forceinline__ MtRange mt_range(const MtArgs &a) {
     return r;
 }
 
-__global__ void __launch_bounds__(kMtThreads) adamw_multi_kernel(const __grid_constant__ Mt32Table T) {
+__global__ void __launch_bounds__(kMtThreads, kMtCtas) adamw_multi_kernel(const __grid_constant__ Mt32Table T) {
     __shared__ MtStep sh;
     MtRange R = mt_range(T.a);
     pdl_wait();
@@ -177,19 +181,29 @@ __device__ __forceinline__ uint32_t e4m3x4_pack(const float *y) {
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
     return lo | (hi << 16);
 }
-// |x| as ordered bits; 0 for infinities and NaN, which set no scale.
-__device__ __forceinline__ uint32_t abs_bits_finite(float x) {
-    const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
-    return b < 0x7f800000u ? b : 0u;
+// One element; x: the restored root of v on entry, the new one on return.
+__device__ __forceinline__ void mt_elem8(float &p, float g, float &m, float &x, const MtArgs &a, const MtStep &s,
+                                         float decay) {
+    m = __fmaf_rn(a.b1, m, __fmul_rn(1.0f - a.b1, g));
+    const float v = __fmaf_rn(a.b2, __fmul_rn(x, x), __fmul_rn(__fmul_rn(1.0f - a.b2, g), g));
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(x) : "f"(v));
+    const float denom = __fmaf_rn(x, s.inv_sqrt_bc2, a.eps);
+    p = __fmaf_rn(-s.step_size, __fdividef(m, denom), __fmul_rn(p, decay));
 }
-// x / b for the code; a non-finite element becomes NaN, so that it stays an
-// element's own fault instead of a saturated value.
-__device__ __forceinline__ float scaled(float x, float b) {
-    const float y = b > 0.f ? __fdiv_rn(x, b) : 0.f;
-    return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u ? __uint_as_float(0x7fffffffu) : y;
+constexpr uint32_t kInfBits = 0x7f800000u;
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// 448 / max and max / 448 of a block; a block whose quotient overflows (max
+// below about 2^-119) is stored as zeros.
+__device__ __forceinline__ void block_scale(uint32_t max_bits, float &inv, float &b) {
+    const float m = __uint_as_float(max_bits);
+    inv = __fdiv_rn(kE4m3Max, m);
+    const bool ok = __float_as_uint(inv) < kInfBits;
+    inv = ok ? inv : 0.f;
+    b = ok ? __fdiv_rn(m, kE4m3Max) : 0.f;
 }
 
-__global__ void __launch_bounds__(kMtThreads) adamw8_multi_kernel(const __grid_constant__ Mt8Table T) {
+__global__ void __launch_bounds__(kMtThreads, kMtCtas) adamw8_multi_kernel(const __grid_constant__ Mt8Table T) {
     static_assert(kBlock8 == 256 && kMtChunk == 8 * kBlock8, "one block per warp and step");
     __shared__ MtStep sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -199,6 +213,7 @@ __global__ void __launch_bounds__(kMtThreads) adamw8_multi_kernel(const __grid_c
     if (threadIdx.x == 0) sh = mt_step(T.a);
     __syncthreads();
     const MtStep S = sh;
+    const float decay = 1.0f - T.a.lr * T.a.wd;
     for (; R.c < R.end; ++R.c) {
         while (R.c >= T.a.chunk0[R.ti + 1]) ++R.ti;
         const qln_adamw8_tensor &t = T.t[R.ti];
@@ -236,20 +251,38 @@ __global__ void __launch_bounds__(kMtThreads) adamw8_multi_kernel(const __grid_c
         uint32_t am = 0, av = 0;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            v[k] = __fmul_rn(v[k], v[k]);
-            v[k] = mt_elem(p[k], g[k], m[k], v[k], T.a, S);  // now sqrt(v)
-            am = max(am, abs_bits_finite(m[k]));
-            av = max(av, abs_bits_finite(v[k]));
+            mt_elem8(p[k], g[k], m[k], v[k], T.a, S, decay);  // v: the root of v
+            am = max(am, abs_bits(m[k]));
+            av = max(av, abs_bits(v[k]));
         }
         am = __reduce_max_sync(0xffffffffu, am);
         av = __reduce_max_sync(0xffffffffu, av);
-        const float nm = __fdiv_rn(__uint_as_float(am), kE4m3Max), nv = __fdiv_rn(__uint_as_float(av), kE4m3Max);
+        const bool odd = max(am, av) >= kInfBits;  // an element is not finite: it sets no scale and becomes NaN
+        if (odd) {
+            am = av = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                am = max(am, abs_bits(m[k]) < kInfBits ? abs_bits(m[k]) : 0u);
+                av = max(av, abs_bits(v[k]) < kInfBits ? abs_bits(v[k]) : 0u);
+            }
+            am = __reduce_max_sync(0xffffffffu, am);
+            av = __reduce_max_sync(0xffffffffu, av);
+        }
+        float im, iv, nm, nv;
+        block_scale(am, im, nm);
+        block_scale(av, iv, nv);
         float ym[8], yv[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            ym[k] = scaled(m[k], nm);
-            yv[k] = scaled(v[k], nv);
-            if (v[k] > 0.f && yv[k] < 0.001953125f) yv[k] = 0.001953125f;  // 2^-9, the smallest code
+            ym[k] = __fmul_rn(m[k], im);
+            yv[k] = fmaxf(__fmul_rn(v[k], iv), v[k] > 0.f ? 0.001953125f : 0.f);  // 2^-9, the smallest code
+        }
+        if (odd) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (abs_bits(m[k]) >= kInfBits) ym[k] = __uint_as_float(0x7fffffffu);
+                if (abs_bits(v[k]) >= kInfBits) yv[k] = __uint_as_float(0x7fffffffu);
+            }
         }
         const uint2 mo = make_uint2(e4m3x4_pack(ym), e4m3x4_pack(ym + 4));
         const uint2 vo = make_uint2(e4m3x4_pack(yv), e4m3x4_pack(yv + 4));
@@ -318,7 +351,7 @@ static cudaError_t launch_multi(void (*kernel)(const Table), const Tensor *tenso
             chunks += (uint64_t)(tensors[i0 + i].n + kMtChunk - 1) / kMtChunk;
         }
         T.a.chunk0[k] = (uint32_t)chunks;
-        const uint64_t wave = (uint64_t)num_sms * 4;
+        const uint64_t wave = (uint64_t)num_sms * kMtCtas;
         e = launch_pdl(kernel, dim3((unsigned)(chunks < wave ? chunks : wave)), dim3(kMtThreads), 0, st, T);
         if (e != cudaSuccess) return e;
     }
