@@ -203,42 +203,73 @@ __device__ __forceinline__ void block_scale(uint32_t max_bits, float &inv, float
     b = ok ? __fdiv_rn(m, kE4m3Max) : 0.f;
 }
 
-__global__ void __launch_bounds__(kMtThreads, kMtCtas) adamw8_multi_kernel(const __grid_constant__ Mt8Table T) {
+// A warp takes one block per step and requests the next one's 2.5 KB before it
+// works on the present one's; a tensor's partial last block is read in its turn.
+constexpr int k8Ctas = 3;
+
+__global__ void __launch_bounds__(kMtThreads, k8Ctas) adamw8_multi_kernel(const __grid_constant__ Mt8Table T) {
     static_assert(kBlock8 == 256 && kMtChunk == 8 * kBlock8, "one block per warp and step");
     __shared__ MtStep sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     MtRange R = mt_range(T.a);
     pdl_wait();
     pdl_trigger();
+    struct Raw {  // this lane's 8 elements of a whole block
+        float4 g[2], p[2];
+        uint2 m, v;
+        float bm, bv;
+    };
+    Raw nxt;
+    uint32_t ac = R.c;  // the look-ahead: its chunk and tensor
+    int ati = R.ti;
+    auto request = [&]() {
+        if (ac < R.end) {
+            while (ac >= T.a.chunk0[ati + 1]) ++ati;
+            const qln_adamw8_tensor &t = T.t[ati];
+            const int64_t blk = (int64_t)(ac - T.a.chunk0[ati]) * (kMtChunk / kBlock8) + warp;
+            if ((blk + 1) * kBlock8 <= t.n) {
+                const int64_t e = blk * kBlock8 + 8 * lane;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    nxt.g[h] = __ldcs(reinterpret_cast<const float4 *>(t.grad + e) + h);
+                    nxt.p[h] = *(reinterpret_cast<const float4 *>(t.param + e) + h);
+                }
+                nxt.m = *reinterpret_cast<const uint2 *>(t.m + e);
+                nxt.v = *reinterpret_cast<const uint2 *>(t.v + e);
+                nxt.bm = t.m_scale[blk];
+                nxt.bv = t.v_scale[blk];
+            }
+        }
+        ++ac;
+    };
+    request();
     if (threadIdx.x == 0) sh = mt_step(T.a);
     __syncthreads();
     const MtStep S = sh;
     const float decay = 1.0f - T.a.lr * T.a.wd;
     for (; R.c < R.end; ++R.c) {
+        const Raw cur = nxt;
+        request();
         while (R.c >= T.a.chunk0[R.ti + 1]) ++R.ti;
         const qln_adamw8_tensor &t = T.t[R.ti];
         const int64_t blk = (int64_t)(R.c - T.a.chunk0[R.ti]) * (kMtChunk / kBlock8) + warp;
         const int64_t e = blk * kBlock8 + 8 * lane;  // this lane's 8 elements
         if (blk * kBlock8 >= t.n) continue;
+        const bool whole = (blk + 1) * kBlock8 <= t.n;
         const int64_t left = t.n - e;
-        const bool full = left >= 8;
-        const float bm = t.m_scale[blk], bv = t.v_scale[blk];
         float p[8], g[8], m[8], v[8];
-        if (full) {
-            const uint2 mc = *reinterpret_cast<const uint2 *>(t.m + e);
-            const uint2 vc = *reinterpret_cast<const uint2 *>(t.v + e);
+        if (whole) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float4 g4 = __ldcs(reinterpret_cast<const float4 *>(t.grad + e) + h);
-                const float4 p4 = *(reinterpret_cast<const float4 *>(t.param + e) + h);
-                g[4 * h] = g4.x, g[4 * h + 1] = g4.y, g[4 * h + 2] = g4.z, g[4 * h + 3] = g4.w;
-                p[4 * h] = p4.x, p[4 * h + 1] = p4.y, p[4 * h + 2] = p4.z, p[4 * h + 3] = p4.w;
+                g[4 * h] = cur.g[h].x, g[4 * h + 1] = cur.g[h].y, g[4 * h + 2] = cur.g[h].z, g[4 * h + 3] = cur.g[h].w;
+                p[4 * h] = cur.p[h].x, p[4 * h + 1] = cur.p[h].y, p[4 * h + 2] = cur.p[h].z, p[4 * h + 3] = cur.p[h].w;
             }
-            e4m3x4_restore(mc.x, bm, m);
-            e4m3x4_restore(mc.y, bm, m + 4);
-            e4m3x4_restore(vc.x, bv, v);
-            e4m3x4_restore(vc.y, bv, v + 4);
+            e4m3x4_restore(cur.m.x, cur.bm, m);
+            e4m3x4_restore(cur.m.y, cur.bm, m + 4);
+            e4m3x4_restore(cur.v.x, cur.bv, v);
+            e4m3x4_restore(cur.v.y, cur.bv, v + 4);
         } else {
+            const float bm = t.m_scale[blk], bv = t.v_scale[blk];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const bool in = k < left;
@@ -286,11 +317,12 @@ __global__ void __launch_bounds__(kMtThreads, kMtCtas) adamw8_multi_kernel(const
         }
         const uint2 mo = make_uint2(e4m3x4_pack(ym), e4m3x4_pack(ym + 4));
         const uint2 vo = make_uint2(e4m3x4_pack(yv), e4m3x4_pack(yv + 4));
+        __syncwarp();  // every lane has read the scales
         if (lane == 0) {
             t.m_scale[blk] = nm;
             t.v_scale[blk] = nv;
         }
-        if (full) {
+        if (whole) {
             *reinterpret_cast<uint2 *>(t.m + e) = mo;
             *reinterpret_cast<uint2 *>(t.v + e) = vo;
 #pragma unroll
@@ -330,8 +362,8 @@ static cudaError_t page_tensor(const qln_adamw8_tensor &t, bool in, int dev, cud
 }
 
 template <typename Table, typename Tensor>
-static cudaError_t launch_multi(void (*kernel)(const Table), const Tensor *tensors, int count, const qln_adamw_config *cfg,
-                                const int64_t *step, int flags, cudaStream_t st, int num_sms) {
+static cudaError_t launch_multi(void (*kernel)(const Table), int ctas, const Tensor *tensors, int count,
+                                const qln_adamw_config *cfg, const int64_t *step, int flags, cudaStream_t st, int num_sms) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -351,7 +383,7 @@ static cudaError_t launch_multi(void (*kernel)(const Table), const Tensor *tenso
             chunks += (uint64_t)(tensors[i0 + i].n + kMtChunk - 1) / kMtChunk;
         }
         T.a.chunk0[k] = (uint32_t)chunks;
-        const uint64_t wave = (uint64_t)num_sms * kMtCtas;
+        const uint64_t wave = (uint64_t)num_sms * ctas;
         e = launch_pdl(kernel, dim3((unsigned)(chunks < wave ? chunks : wave)), dim3(kMtThreads), 0, st, T);
         if (e != cudaSuccess) return e;
     }
@@ -363,11 +395,11 @@ static cudaError_t launch_multi(void (*kernel)(const Table), const Tensor *tenso
 
 cudaError_t launch_adamw_multi(const qln_adamw_tensor *t, int count, const qln_adamw_config *cfg, const int64_t *step,
                                int flags, cudaStream_t st, int num_sms) {
-    return launch_multi<Mt32Table>(adamw_multi_kernel, t, count, cfg, step, flags, st, num_sms);
+    return launch_multi<Mt32Table>(adamw_multi_kernel, kMtCtas, t, count, cfg, step, flags, st, num_sms);
 }
 cudaError_t launch_adamw8_multi(const qln_adamw8_tensor *t, int count, const qln_adamw_config *cfg, const int64_t *step,
                                 int flags, cudaStream_t st, int num_sms) {
-    return launch_multi<Mt8Table>(adamw8_multi_kernel, t, count, cfg, step, flags, st, num_sms);
+    return launch_multi<Mt8Table>(adamw8_multi_kernel, k8Ctas, t, count, cfg, step, flags, st, num_sms);
 }
 
 }  // namespace qln
