@@ -64,12 +64,16 @@ constexpr int kBM = 128;   // rows per accumulator (TMEM lanes)
 constexpr int kBK = 64;
 constexpr uint64_t kWaitLimitNs = 4000000000ull;  // 4 s
 
-template <int MT, int NT>
+template <int MT, int NT, bool MULTI>
 struct Cfg {
     static_assert(MT * NT <= 2, "two TMEM accumulators of up to 256 columns at most");
     static constexpr int kStages = MT * NT == 1 ? 4 : 3;
     static constexpr int kMaxBN = NT == 1 ? 256 : 208;     // tokens per accumulator
-    static constexpr int kDecThreads = 128 * MT;
+    // One decoder per 64-wide row block of the weight tile; MULTI: always 256, so that with MT = 1 two threads share a
+    // block.  One warp per scheduler decodes at a third of its issue rate; with two, K steps of few tokens, which the
+    // decoding bounds, take XX % less.
+    static constexpr int kDecThreads = MULTI ? 256 : 128 * MT;
+    static constexpr int kShare = kDecThreads / (128 * MT);  // threads per block
     static constexpr int kThreads = 64 + kDecThreads;
     static constexpr uint32_t kABytes = 16384u * MT;        // MT x (128 rows x 64 K) bf16
     static constexpr uint32_t kBBytes = NT * kMaxBN * kBK * 2;
@@ -81,6 +85,7 @@ struct Cfg {
     static constexpr uint32_t kOffBar = kOffC + kStages * kCBytes;
     // barriers: tma_full[S], code_full[S], dec_full[S], empty[S], accum_full, list_full (MULTI)
     static constexpr uint32_t kNumBars = 4 * kStages + 2;
+    static_assert(MT * NT == 1 || kOffBar == 221184u, "one size for both");
     static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;  // tmem base, abort flag, epilogue go
     static constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;  // + alignment slack
     // MULTI: the tile's list of adapters (one word each), the adapter of each token, and the list's place of every
@@ -99,6 +104,22 @@ struct MultiParams {
     const uint16_t *lw;    // the pool's factors
     int count, r;
 };
+
+// ---- cluster (K split of a MULTI call) ----
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_map(uint32_t saddr, uint32_t rank) {
+    uint32_t d;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(saddr), "r"(rank));
+    return d;
+}
+__device__ __forceinline__ void cluster_st_u32(uint32_t a, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
+// Columns (tokens) of a tile that each CTA of a K split finishes: a multiple of 8.
+__host__ __device__ constexpr int split_cols(int ntok, int ks) { return ((ntok + ks - 1) / ks + 7) & ~7; }
 
 // What the products of a factor's non-finite elements add to one output (m, t)
 // of adapter a: lw rows of m with stride 1 over j (forward) or columns with
@@ -130,11 +151,11 @@ struct Params {
 };
 
 template <bool TRANS, int MT, int NT, bool MULTI>
-__global__ void __launch_bounds__(Cfg<MT, NT>::kThreads, 1)
+__global__ void __launch_bounds__(Cfg<MT, NT, MULTI>::kThreads, 1)
 nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_act,
                    const __grid_constant__ CUtensorMap tm_lw, const __grid_constant__ CUtensorMap tm_lact,
                    const Params p, const __grid_constant__ MultiParams mp) {
-    using C = Cfg<MT, NT>;
+    using C = Cfg<MT, NT, MULTI>;
     constexpr int S = C::kStages;
     constexpr int TM = kBM * MT;  // rows of the CTA tile
     extern __shared__ uint8_t smem_raw[];
@@ -154,7 +175,11 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t0 = (int64_t)blockIdx.x * NT * p.BN;  // NT accumulators of BN tokens each
     const int64_t m0 = (int64_t)blockIdx.y * TM;
-    const int nsteps = p.KT + (MULTI ? 0 : p.RT);
+    // MULTI: the cluster's CTAs share the K steps (and the steps of chunks) of one tile
+    const int ks = MULTI ? (int)gridDim.z : 1, kz = MULTI ? (int)blockIdx.z : 0;
+    const int k0 = MULTI ? p.KT * kz / ks : 0;                              // this CTA's first weight step
+    const int nweight = MULTI ? p.KT * (kz + 1) / ks - k0 : p.KT;           // and how many it has
+    const int nsteps = nweight + (MULTI ? 0 : p.RT);
     // MULTI: the tile's adapters
     uint32_t *s_list = reinterpret_cast<uint32_t *>(smem + C::kOffList);  // adapter | rank << 12 | sub-tiles << 24
     int16_t *s_tok = reinterpret_cast<int16_t *>(s_list + C::kTok);
@@ -164,7 +189,7 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
     // The chunks in their order, for a whole warp.  A batch covers E = 2^k entries of the list (all of them, up to 32)
     // and 32 / E columns-of-16; lane i holds its i-th chunk: entry | (first column / 16) << 26.
     struct Chunks {
-        int na, E, e0, j0, cnt, pos;
+        int na, E, e0, j0, cnt, pos, batch, step;  // batch: its number; step: of all steps of chunks
         uint32_t d, mask;  // mask: which of the batch's E x 32 / E places are chunks
     };
     auto refill = [&](Chunks &k) -> bool {  // to the next batch with a chunk; false past the last
@@ -187,6 +212,7 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
             k.mask = mask;
             k.cnt = __popc(mask);
             k.pos = 0;
+            ++k.batch;
             return true;
         }
     };
@@ -194,7 +220,7 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
         k.na = *s_count;
         k.E = k.na <= 1 ? 1 : (k.na > 16 ? 32 : 1 << (32 - __clz(k.na - 1)));
         k.e0 = -k.E;
-        k.j0 = 0;
+        k.j0 = k.batch = k.step = 0;
         return k.na > 0 && refill(k);
     };
     auto take = [&](Chunks &k, uint32_t (&ent)[4]) -> bool {  // the next step's chunks (0: none); whether more follow
@@ -204,7 +230,16 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
             ent[q] = k.pos + q < k.cnt ? d : 0u;
         }
         k.pos += 4;
+        ++k.step;
         return k.pos < k.cnt || refill(k);
+    };
+    auto skip = [&](Chunks &k, bool more) -> bool {  // past the steps of the cluster's other CTAs
+        while (more && k.step % ks != kz) {
+            ++k.step;
+            k.pos += 4;
+            more = k.pos < k.cnt || refill(k);
+        }
+        return more;
     };
     auto ent_who = [](uint32_t d) { return (int)(d & 0xfffu); };
     auto ent_col = [](uint32_t d) { return (int)(d >> 26) * 16; };
@@ -269,19 +304,19 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                 const uint32_t sA = sbase + C::kOffA + s * C::kABytes;
                 const uint32_t sB = sbase + C::kOffB + s * C::kBBytes;
                 const uint32_t sC = sbase + C::kOffC + s * C::kCBytes;
-                if (kt < p.KT) {
+                if (kt < nweight) {
                     mbar_arrive_expect_tx(code_full(s), C::kCBytes);
                     if (!TRANS) {  // TM rows x 32 bytes
-                        tma_load_2d(sC, &tm_codes, kt * 32, (int32_t)m0, code_full(s));
+                        tma_load_2d(sC, &tm_codes, (k0 + kt) * 32, (int32_t)m0, code_full(s));
                     } else {       // 2*MT boxes of 64 rows x 32 bytes: [column block][row][32 B]
 #pragma unroll
                         for (int d = 0; d < 2 * MT; ++d)
-                            tma_load_2d(sC + 2048 * d, &tm_codes, (int32_t)(m0 / 2) + 32 * d, kt * kBK, code_full(s));
+                            tma_load_2d(sC + 2048 * d, &tm_codes, (int32_t)(m0 / 2) + 32 * d, (k0 + kt) * kBK, code_full(s));
                     }
                     mbar_arrive_expect_tx(tma_full(s), bbytes);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
-                        tma_load_2d(sB + nt * bsub, &tm_act, kt * kBK, (int32_t)(t0 + nt * p.BN), tma_full(s));
+                        tma_load_2d(sB + nt * bsub, &tm_act, (k0 + kt) * kBK, (int32_t)(t0 + nt * p.BN), tma_full(s));
                 } else {
                     const int a = kt - p.KT;
                     mbar_arrive_expect_tx(tma_full(s), C::kABytes + bbytes);
@@ -311,7 +346,7 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
             __syncwarp();  // the list, which lane 0 has waited for
             Chunks k;
             bool more = __shfl_sync(0xffffffffu, ok, 0) && begin(k);
-            while (more) {
+            while ((more = skip(k, more))) {
                 const int s = issued % S;
                 const uint32_t sA = sbase + C::kOffA + s * C::kABytes;
                 uint32_t ent[4];
@@ -346,7 +381,7 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                 const int s = kt % S;
                 const uint32_t ph = (uint32_t)(kt / S) & 1u;
                 if (!mbar_wait_bounded(tma_full(s), ph, nullptr, kWaitLimitNs)) give_up();
-                if (kt < p.KT && !mbar_wait_bounded(code_full(s), ph, nullptr, kWaitLimitNs)) give_up();
+                if (kt < nweight && !mbar_wait_bounded(code_full(s), ph, nullptr, kWaitLimitNs)) give_up();
             }
         }
     } else if (warp == 1) {
@@ -390,19 +425,23 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
             }
             __syncwarp();
         }
-        if (lane == 0) {
-            const uint32_t idesc = idesc_bf16_f32(kBM, p.BN, TRANS, false);
-            for (int kt = 0; kt < nsteps; ++kt) {
-                const int s = kt % S;
-                const uint32_t ph = (uint32_t)(kt / S) & 1u;
-                if (!mbar_wait_bounded(tma_full(s), ph, abort_flag, kWaitLimitNs) ||
-                    !mbar_wait_bounded(dec_full(s), ph, abort_flag, kWaitLimitNs)) {
-                    give_up();
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t sA = sbase + C::kOffA + s * C::kABytes;
-                const uint32_t sB = sbase + C::kOffB + s * C::kBBytes;
+        // The whole warp runs the loop and one lane issues: the descriptors are warp-uniform values then, which is how the
+        // instruction takes them.
+        const uint32_t idesc = idesc_bf16_f32(kBM, p.BN, TRANS, false);
+        const uint64_t adesc0 = smem_desc_sw128(sbase + C::kOffA, TRANS ? 8192 : 16, 1024);
+        const uint64_t bdesc0 = smem_desc_sw128(sbase + C::kOffB, 16, 1024);
+        int s = 0;
+        uint32_t ph = 0;
+        for (int kt = 0; kt < nsteps; ++kt) {
+            const bool ok = mbar_wait_bounded(tma_full(s), ph, abort_flag, kWaitLimitNs) &&
+                            mbar_wait_bounded(dec_full(s), ph, abort_flag, kWaitLimitNs);
+            if (!__all_sync(0xffffffffu, ok)) {
+                if (lane == 0) give_up();
+                break;
+            }
+            tc_fence_after();
+            const uint64_t ad = adesc0 + (uint32_t)s * (C::kABytes >> 4), bd = bdesc0 + (uint32_t)s * (C::kBBytes >> 4);
+            if (lane == 0) {
 #pragma unroll
                 for (int sub = 0; sub < MT; ++sub) {
 #pragma unroll
@@ -411,23 +450,24 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                         for (int k = 0; k < kBK / 16; ++k) {
                             // K-major: next 16 K elements are 32 bytes further inside the
                             // swizzled 128-byte rows.  MN-major: next two 8-row K groups.
-                            const uint32_t aS = sA + sub * 16384;
-                            const uint64_t adesc = TRANS ? smem_desc_sw128(aS + k * 2048, 8192, 1024)
-                                                         : smem_desc_sw128(aS + k * 32, 16, 1024);
-                            const uint64_t bdesc = smem_desc_sw128(sB + nt * p.BN * 128 + k * 32, 16, 1024);
-                            tc_mma_ss(tmem_d + (sub * NT + nt) * 256, adesc, bdesc, idesc, (kt | k) != 0 ? 1u : 0u);
+                            tc_mma_ss(tmem_d + (sub * NT + nt) * 256, ad + ((sub * 16384 + k * (TRANS ? 2048 : 32)) >> 4),
+                                      bd + (uint32_t)(nt * p.BN * 8) + (k * 32 >> 4), idesc, (kt | k) != 0 ? 1u : 0u);
                         }
                     }
                 }
                 tc_commit(empty(s));
             }
+            __syncwarp();
+            if (++s == S) {
+                s = 0;
+                ph ^= 1u;
+            }
         }
         if constexpr (MULTI) {
-            const uint32_t idesc = idesc_bf16_f32(kBM, p.BN, TRANS, false);
             __syncwarp();
             Chunks k;
             bool more = begin(k);
-            for (int kt = nsteps; more; ++kt) {
+            for (int kt = nsteps; (more = skip(k, more)); ++kt) {
                 const int s = kt % S;
                 const uint32_t ph = (uint32_t)(kt / S) & 1u;
                 uint32_t ent[4];
@@ -471,8 +511,9 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
         //   dX : block = W row 64*kt + dt%64, column block m0/64 + dt/64.
         const int dt = threadIdx.x - 64;
         const int64_t bpr = p.cols / 64;
-        const int drow = TRANS ? (dt & 63) : dt;
-        const int dcol = TRANS ? (dt >> 6) : 0;
+        const int db = dt & (128 * MT - 1), share = dt / (128 * MT);  // block, and which of its threads
+        const int drow = TRANS ? (db & 63) : db;
+        const int dcol = TRANS ? (db >> 6) : 0;
         const float mu = p.qabs ? __ldg(p.dq_mean) : 0.f;
         auto block_index = [&](int kt) -> int64_t {
             return TRANS ? ((int64_t)kt * kBK + drow) * bpr + (m0 / 64) + dcol : (m0 + drow) * bpr + kt;
@@ -485,8 +526,8 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
         };
         auto fetch = [&](int kt) -> Raw {
             Raw r{0.f, 0};
-            if (kt < p.KT) {
-                const int64_t jb = block_index(kt);
+            if (kt < nweight) {
+                const int64_t jb = block_index(k0 + kt);
                 if (p.qabs) {
                     r.q = __ldg(p.qabs + jb);
                     r.v = __ldg(p.dq_scale + (jb >> 8));
@@ -521,25 +562,36 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                 give_up();
                 break;
             }
-            if (kt < p.KT) {
+            if (kt < nweight) {
                 if (!mbar_wait_bounded(code_full(s), ph, abort_flag, kWaitLimitNs)) {
                     give_up();
                     break;
                 }
                 const uint8_t *cptr = smem + C::kOffC + s * C::kCBytes + code_off;
-                const uint4 ca = *reinterpret_cast<const uint4 *>(cptr + 16 * cfirst);
-                const uint4 cb = *reinterpret_cast<const uint4 *>(cptr + 16 * (cfirst ^ 1));
-                const NF4Table tab = nf4_table(ah);
-                const uint32_t xa = (sA0 + s * C::kABytes) ^ (cfirst << 6);  // chunks of ca: 4*cfirst + i
-                const uint32_t xb = xa ^ 64u;                                  // chunks of cb
-                st_shared_v4(xa ^ 0u, nf4_decode8(ca.x, tab));
-                st_shared_v4(xa ^ 16u, nf4_decode8(ca.y, tab));
-                st_shared_v4(xa ^ 32u, nf4_decode8(ca.z, tab));
-                st_shared_v4(xa ^ 48u, nf4_decode8(ca.w, tab));
-                st_shared_v4(xb ^ 0u, nf4_decode8(cb.x, tab));
-                st_shared_v4(xb ^ 16u, nf4_decode8(cb.y, tab));
-                st_shared_v4(xb ^ 32u, nf4_decode8(cb.z, tab));
-                st_shared_v4(xb ^ 48u, nf4_decode8(cb.w, tab));
+                if constexpr (C::kShare == 1) {
+                    const uint4 ca = *reinterpret_cast<const uint4 *>(cptr + 16 * cfirst);
+                    const uint4 cb = *reinterpret_cast<const uint4 *>(cptr + 16 * (cfirst ^ 1));
+                    const NF4Table tab = nf4_table(ah);
+                    const uint32_t xa = (sA0 + s * C::kABytes) ^ (cfirst << 6);  // chunks of ca: 4*cfirst + i
+                    const uint32_t xb = xa ^ 64u;                                  // chunks of cb
+                    st_shared_v4(xa ^ 0u, nf4_decode8(ca.x, tab));
+                    st_shared_v4(xa ^ 16u, nf4_decode8(ca.y, tab));
+                    st_shared_v4(xa ^ 32u, nf4_decode8(ca.z, tab));
+                    st_shared_v4(xa ^ 48u, nf4_decode8(ca.w, tab));
+                    st_shared_v4(xb ^ 0u, nf4_decode8(cb.x, tab));
+                    st_shared_v4(xb ^ 16u, nf4_decode8(cb.y, tab));
+                    st_shared_v4(xb ^ 32u, nf4_decode8(cb.z, tab));
+                    st_shared_v4(xb ^ 48u, nf4_decode8(cb.w, tab));
+                } else {  // half of the block: the one read first or second above
+                    const uint32_t half = cfirst ^ (uint32_t)share;
+                    const uint4 ca = *reinterpret_cast<const uint4 *>(cptr + 16 * half);
+                    const NF4Table tab = nf4_table(ah);
+                    const uint32_t xa = (sA0 + s * C::kABytes) ^ (half << 6);
+                    st_shared_v4(xa ^ 0u, nf4_decode8(ca.x, tab));
+                    st_shared_v4(xa ^ 16u, nf4_decode8(ca.y, tab));
+                    st_shared_v4(xa ^ 32u, nf4_decode8(ca.z, tab));
+                    st_shared_v4(xa ^ 48u, nf4_decode8(ca.w, tab));
+                }
                 fence_proxy_async_smem();
             }
             mbar_arrive(dec_full(s));
@@ -552,7 +604,7 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
             // theirs, as its place and its number (kNone: none left); and the chunks of each stage that hold values of
             // them (4 bits a stage).
             constexpr int kNone = 1 << 20;
-            int place[kRows], at[kRows], num[kRows];
+            int place[kRows], at[kRows], num[kRows], batch = -1;
             uint32_t held[kRows];
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
@@ -570,7 +622,8 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
             auto put = [&](int kt) {
                 const int s = kt % S, step = k.pos >> 2;
                 const uint32_t sB = sbase + C::kOffB + s * C::kBBytes;
-                if (k.pos == 0) {
+                if (batch != k.batch) {
+                    batch = k.batch;
 #pragma unroll
                     for (int i = 0; i < kRows; ++i) {
                         const int to = place[i] - k.e0;
@@ -584,6 +637,7 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                     uint32_t old = (held[i] >> (4 * s)) & 15u, now = 0u;
                     if (kt - nsteps < S) old = row < NT * p.BN ? 15u : 0u;
                     const uint32_t to = sB + row * 32 + (((row >> 2) & 1) << 4);  // 32-byte swizzle: halves at `to` and to ^ 16
+                    while ((num[i] >> 2) < step) seek(i, at[i] + k.E);  // chunks of the cluster's other CTAs
                     while ((num[i] >> 2) == step) {
                         const int q = num[i] & 3, j = k.j0 + 16 * (at[i] / k.E);
                         const uint16_t *src = mp.lact + (t0 + row) * mp.r + j;
@@ -615,6 +669,7 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
             uint32_t ent[4] = {0u, 0u, 0u, 0u}, nxt[4] = {0u, 0u, 0u, 0u};
             int nq = 0, nxq = 0;
             bool more = __all_sync(0xffffffffu, !*abort_flag) && begin(k);
+            more = skip(k, more);
             auto advance = [&](int kt) -> bool {  // puts step kt and moves on
                 if (!free_stage(kt)) return false;
                 put(kt);
@@ -623,8 +678,10 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                     more = take(k, nxt);
                 } else {
                     k.pos += 4;
+                    ++k.step;
                     more = k.pos < k.cnt || refill(k);
                 }
+                more = skip(k, more);
                 return true;
             };
             bool live = more && advance(nsteps);
@@ -665,49 +722,53 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                 };
                 bool bad = false;
                 if (!TRANS) {
-                    // row dt: its two 16-byte halves change places where bit 7 of the address is set
-                    uint4 *row = reinterpret_cast<uint4 *>(sA + dt * 32);
+                    // row drow: its two 16-byte halves change places where bit 7 of the address is set; the threads of
+                    // a row share its chunks
+                    constexpr int kQ = 4 / C::kShare;
+                    const int q0 = share * kQ;
+                    uint4 *row = reinterpret_cast<uint4 *>(sA + q0 * kAChunk + drow * 32);
                     if (mp.rank) {
-                        const int swap = (dt >> 2) & 1;
+                        const int swap = (drow >> 2) & 1;
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            for (int h = ent[q] ? ent_left(ent[q]) : 16; h < 16; ++h)
-                                reinterpret_cast<uint16_t *>(row + q * (kAChunk / 16) + ((h >> 3) ^ swap))[h & 7] = 0;
+                            for (int h = ent[q] && q / kQ == share ? ent_left(ent[q]) : 16; h < 16; ++h)
+                                reinterpret_cast<uint16_t *>(row + (q % kQ) * (kAChunk / 16) + ((h >> 3) ^ swap))[h & 7] = 0;
                     }
-                    uint4 v[4][2];
+                    uint4 v[kQ][2];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
+                    for (int q = 0; q < kQ; ++q)
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
-                            v[q][h] = q < nq ? row[q * (kAChunk / 16) + h] : make_uint4(0u, 0u, 0u, 0u);
+                            v[q][h] = q0 + q < nq ? row[q * (kAChunk / 16) + h] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = 0; q < kQ; ++q) {
                         look(v[q][0]);
                         look(v[q][1]);
                     }
                     if (is_odd(odd())) {
                         bad = true;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            if (q < nq) clear(row + q * (kAChunk / 16), 2);
+                        for (int q = 0; q < kQ; ++q)
+                            if (q0 + q < nq) clear(row + q * (kAChunk / 16), 2);
                     }
                 } else {
+                    constexpr int kV = 8 / C::kShare;  // of a row's eight 16-byte pieces
                     const int q = drow >> 4;
                     uint4 *row = reinterpret_cast<uint4 *>(sA + dcol * 8192 + drow * 128);
                     const uint32_t e = q == 0 ? ent[0] : q == 1 ? ent[1] : q == 2 ? ent[2] : ent[3];
                     if (q < nq) {
                         if (mp.rank && (drow & 15) >= ent_left(e)) {  // past the rank
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) row[c ^ r8] = make_uint4(0u, 0u, 0u, 0u);
+                            for (int c = 0; c < kV; ++c) row[(share * kV + c) ^ r8] = make_uint4(0u, 0u, 0u, 0u);
                         } else {
-                            uint4 v[8];
+                            uint4 v[kV];
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) v[c] = row[c ^ r8];
+                            for (int c = 0; c < kV; ++c) v[c] = row[(share * kV + c) ^ r8];
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) look(v[c]);
+                            for (int c = 0; c < kV; ++c) look(v[c]);
                             if (is_odd(odd())) {
                                 bad = true;
-                                clear(row, 8);
+                                for (int c = 0; c < kV; ++c) clear(row + ((share * kV + c) ^ r8), 1);
                             }
                         }
                     }
@@ -726,15 +787,17 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
         asm volatile("bar.sync 1, %0;" ::"n"(C::kDecThreads) : "memory");
         if (dt == 0) *epi_go = *abort_flag ? 0 : 1;
         asm volatile("bar.sync 1, %0;" ::"n"(C::kDecThreads) : "memory");
-        if (*epi_go) {
+        if (*epi_go && ks == 1) {
             tc_fence_after();
             const int q = warp & 3;              // TMEM lane quadrant of this warp
-            const int sub = (warp - 2) >> 2;     // weight sub-tile of this warp
+            const int sub = C::kShare == 1 ? (warp - 2) >> 2 : 0;   // weight sub-tile of this warp
+            const int part = C::kShare == 1 ? 0 : (warp - 2) >> 2;  // or which of the two warps of a quadrant it is
             uint16_t *Os = reinterpret_cast<uint16_t *>(smem);  // [NT*BN][TM] bf16; all MMAs are done
             const int m = sub * kBM + q * 32 + lane;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 for (int c0 = 0; c0 < p.BN; c0 += 32) {
+                    if (C::kShare == 2 && ((nt + c0 / 32) & 1) != part) continue;
                     uint32_t v[32];
                     tmem_ld_32x32b_x32(tmem_d + ((uint32_t)(q * 32) << 16) + (uint32_t)((sub * NT + nt) * 256 + c0), v);
                     tmem_wait_ld();
@@ -749,9 +812,8 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                 if (*s_bad) {  // once more, with the products of the factors' non-finite elements
                     qln::pdl_wait();
                     for (int k = 0; k < NT * p.BN; ++k) {
-                        const int a = s_tok[k];
-                        if (a < 0) continue;
-                        const int nt = k / p.BN;
+                        const int a = s_tok[k], nt = k >= p.BN ? 1 : 0;
+                        if (a < 0 || (C::kShare == 2 && ((nt + (k - nt * p.BN) / 32) & 1) != part)) continue;
                         uint32_t v;
                         asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];"
                                      : "=r"(v)
@@ -771,6 +833,61 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                 if (t < p.n)
                     *reinterpret_cast<uint4 *>(p.out + t * p.out_ld + m0 + 8 * ch) =
                         *reinterpret_cast<const uint4 *>(Os + row * TM + 8 * ch);
+            }
+        }
+    }
+
+    // K split: CTA q of the cluster finishes every cq-th part of the tile's columns (tokens).  Every CTA sends its
+    // accumulators there (fp32, into the stages, which nobody uses any more), and they are added in the CTAs' order.
+    if constexpr (MULTI) {
+        if (ks > 1) {
+            const int ntok = NT * p.BN, cq = split_cols(ntok, ks), c_lo = kz * cq, c_n = min(cq, ntok - c_lo);
+            __syncthreads();
+            const bool go = *epi_go != 0;
+            cluster_sync();  // every CTA's copies have landed, its MMAs have retired
+            if (warp >= 2 && go) {
+                // Eight columns at a time in a short loop: this code runs once, and unrolled over 32 columns its
+                // instructions took longer to fetch (8 us) than its data to move.
+                tc_fence_after();
+                const int q = warp & 3, sub = C::kShare == 1 ? (warp - 2) >> 2 : 0, part = C::kShare == 1 ? 0 : (warp - 2) >> 2;
+                const uint32_t mine = sbase + (uint32_t)((kz * cq) * TM + sub * kBM + q * 32 + lane) * 4u;
+#pragma unroll 1
+                for (int col = 8 * part; col < ntok; col += 8 * C::kShare) {
+                    const int nt = NT == 2 && col >= p.BN ? 1 : 0, to = col / cq;
+                    uint32_t v[8];
+                    tmem_ld_32x32b_x8(tmem_d + ((uint32_t)(q * 32) << 16) + (uint32_t)((sub * NT + nt) * 256 + col - nt * p.BN), v);
+                    const uint32_t d = cluster_map(mine + (uint32_t)((col - to * cq) * TM) * 4u, (uint32_t)to);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) cluster_st_u32(d + j * TM * 4u, v[j]);
+                }
+                tc_fence_before();
+                if (threadIdx.x == 64 && *s_bad)
+                    for (int z = 0; z < ks; ++z)
+                        cluster_st_u32(cluster_map(smem_addr(const_cast<const int *>(s_bad)), (uint32_t)z), 1u);
+            }
+            __syncwarp();
+            cluster_sync();  // all parts are here
+            if (warp >= 2 && go) {
+                const float *part_s = reinterpret_cast<const float *>(smem);
+                const bool bad = *s_bad != 0;
+                constexpr int kCh = TM / 8;
+                for (int idx = threadIdx.x - 64; idx < c_n * kCh; idx += C::kDecThreads) {
+                    const int col = idx / kCh, m = (idx % kCh) * 8, k = c_lo + col;
+                    const int64_t t = t0 + k;
+                    if (t >= p.n) continue;
+                    float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    for (int z = 0; z < ks; ++z) {
+                        const float4 *src = reinterpret_cast<const float4 *>(part_s + (z * cq + col) * TM + m);
+                        const float4 u = src[0], w = src[1];
+                        y[0] += u.x, y[1] += u.y, y[2] += u.z, y[3] += u.w;
+                        y[4] += w.x, y[5] += w.y, y[6] += w.z, y[7] += w.w;
+                    }
+                    if (bad && s_tok[k] >= 0)
+                        for (int j = 0; j < 8; ++j) y[j] += nonfinite_products(mp, s_tok[k], m0 + m + j, t, p.out_ld, TRANS);
+                    *reinterpret_cast<uint4 *>(p.out + t * p.out_ld + m0 + m) =
+                        make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+                }
             }
         }
     }
@@ -881,14 +998,72 @@ static TileShape choose_shape(int64_t M, int64_t K, int64_t n, int num_sms) {
     return best;
 }
 
+// Tile shape and K split of a MULTI call.  A k-step takes 1200 cycles at least (its chain of copy, decoding and MMA
+// through the ring; 1600 with MT = 2), and 1.25 (1.35) times its tensor time where that is more; a tile takes 4000
+// cycles besides, and a split 6000 more for the exchange.  Splitting fills the SMs where there are few tiles:
+// 4096 x 4096 and 333 tokens, rank 8, take XX us split in four, YY us unsplit.
+struct MultiShape {
+    TileShape t;
+    int ks;
+};
+
+static MultiShape choose_multi(int64_t M, int64_t K, int64_t n, int num_sms) {
+    const int KT = (int)(K / kBK);
+    MultiShape best{{1, 1, 128}, 1};
+    double best_cost = 1e300;
+    const int shapes[3][2] = {{2, 1}, {1, 2}, {1, 1}};
+    for (const auto &sh : shapes) {
+        const int MT = sh[0], NT = sh[1];
+        if ((M % (kBM * MT)) != 0) continue;
+        for (int bn = NT == 1 ? 256 : 208; bn >= 16; bn -= 16) {
+            if (bn < 128 && (int64_t)NT * bn < n) break;  // narrow tiles only for small n
+            const int64_t tok = (int64_t)NT * bn, ttiles = (n + tok - 1) / tok, tiles = ttiles * (M / (kBM * MT));
+            for (int ks = 1; ks <= 4; ++ks) {
+                // the exchange takes the stages' shared memory
+                const int64_t room = MT * NT == 2 ? Cfg<2, 1, true>::kOffBar : Cfg<1, 1, true>::kOffBar;
+                if (ks > 1 && (ks * 4 > KT || (int64_t)ks * split_cols((int)tok, ks) * kBM * MT * 4 > room)) continue;
+                // CTAs that run at once: a cluster stays within one of 8 groups of about 18 SMs
+                const int64_t slots = ks == 1 ? num_sms : (int64_t)8 * (18 / ks) * ks;
+                const int64_t rounds = (tiles * ks + slots - 1) / slots;
+                const double mma = (MT == 2 ? 1.35 : 1.25) * 2.0 * kBM * MT * (double)tok * kBK / 5700.0;
+                const double least = MT == 2 ? 1600.0 : 1200.0;
+                const double cost = rounds * (((KT + ks - 1) / ks + 1) * ((mma > least ? mma : least) + 0.15 * mma) + 4000.0 + (ks > 1 ? 6000.0 : 0.0)) *
+                                    (1.0 + 1e-4 * (double)(ttiles * tok - n) / (double)n);
+                if (cost < best_cost * 0.999) {
+                    best_cost = cost;
+                    best = MultiShape{{MT, NT, bn}, ks};
+                }
+            }
+        }
+    }
+    return best;
+}
+
 template <bool TRANS, int MT, int NT, bool MULTI>
 static cudaError_t launch_t(const CUtensorMap &m_codes, const CUtensorMap &m_act, const CUtensorMap &m_lw,
                             const CUtensorMap &m_lact, const Params &p, const MultiParams &mp, dim3 grid, cudaStream_t st) {
-    using C = Cfg<MT, NT>;
+    using C = Cfg<MT, NT, MULTI>;
     constexpr uint32_t smem = MULTI ? C::kSmemBytesMulti : C::kSmemBytes;
     cudaError_t e = cudaFuncSetAttribute(nf4_tc_gemm_kernel<TRANS, MT, NT, MULTI>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
+    if (MULTI && grid.z > 1) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = grid.z;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3(C::kThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        qln::note_launch();
+        return cudaLaunchKernelEx(&cfg, nf4_tc_gemm_kernel<TRANS, MT, NT, MULTI>, m_codes, m_act, m_lw, m_lact, p, mp);
+    }
     return qln::launch_pdl(nf4_tc_gemm_kernel<TRANS, MT, NT, MULTI>, grid, dim3(C::kThreads), (size_t)smem, st,
                            m_codes, m_act, m_lw, m_lact, p, mp);
 }
@@ -936,7 +1111,9 @@ static cudaError_t launch_tc(const qln_nf4_weight *w, bool trans, const uint16_t
     const int64_t rows = w->rows, cols = w->cols;
     const int64_t M = trans ? cols : rows;
     const int64_t K = trans ? rows : cols;
-    const TileShape shape = choose_shape(M, K, n, num_sms > 0 ? num_sms : 148);
+    const MultiShape ms = view ? choose_multi(M, K, n, num_sms > 0 ? num_sms : 148)
+                               : MultiShape{choose_shape(M, K, n, num_sms > 0 ? num_sms : 148), 1};
+    const TileShape shape = ms.t;
     const int NT = shape.NT, BN = shape.BN;
     const int TM = kBM * shape.MT;
     CUtensorMap m_codes, m_act, m_lw, m_lact;
@@ -974,7 +1151,7 @@ static cudaError_t launch_tc(const qln_nf4_weight *w, bool trans, const uint16_t
     p.KT = (int)(K / kBK);
     p.RT = (r + kBK - 1) / kBK;
     p.BN = BN;
-    dim3 grid((unsigned)((n + (int64_t)NT * BN - 1) / ((int64_t)NT * BN)), (unsigned)(M / TM));
+    dim3 grid((unsigned)((n + (int64_t)NT * BN - 1) / ((int64_t)NT * BN)), (unsigned)(M / TM), (unsigned)ms.ks);
     if (!view) return launch_shape<false>(trans, shape, m_codes, m_act, m_lw, m_lact, p, MultiParams{}, grid, st);
     const MultiParams mp{view->ids, view->rank, lact, lw, view->count, r};
     return launch_shape<true>(trans, shape, m_codes, m_act, m_lw, m_lact, p, mp, grid, st);

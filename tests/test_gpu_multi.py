@@ -310,8 +310,11 @@ def test_one_adapter_agrees_with_the_single_adapter_call():
 
 def test_adapters_train_together_and_serve():
     """As they are used: three adapters trained in one batch (forward, backward, the 8-bit AdamW step over all factors),
-    the updated pool then serving single tokens.  The step's parameters agree with the 32-bit step's, since both start
-    from zero states: the update of step one uses states that have not been rounded yet."""
+    the updated pool then serving single tokens.  The step's parameters agree with the 32-bit step's up to fp32
+    rounding, since both start from zero states and the update uses states that have not been rounded to 8 bits yet:
+    step one moves a parameter by at most lr (m / d S = lr g / (|g| + eps')), which the 32-bit kernel forms within
+    10 units of 2^-24 and the 8-bit one within 16 (its root and quotient are the hardware's approximate ones); the decay
+    is 1 here, and both round the difference p' once: 26 u lr + 2 u |p'|."""
     c = Case(256, 512, 150, 3, 16, "blocks", seed=2)
     masters = [c.A.float(), c.B.float()]
     other = [m.clone() for m in masters]
@@ -328,7 +331,8 @@ def test_adapters_train_together_and_serve():
     api.adamw8_multi_step(t8, step, 1e-2)
     api.adamw_multi_step(t32, step, 1e-2)
     torch.cuda.synchronize()
-    assert all(torch.equal(a, b) for a, b in zip(masters, other))
+    for a, b in zip(masters, other):
+        _near("parameters", a, b.double(), 2.0 ** -24 * (26 * 1e-2 + 2 * b.double().abs()))
     assert torch.equal(c.A, masters[0].bfloat16()) and torch.equal(c.B, masters[1].bfloat16())
     assert not torch.equal(c.A, before[0]) and not torch.equal(c.B, before[1])
     X, ids = c.X[:9].contiguous(), torch.tensor([0, 1, 2, -1, 2, 1, 0, 0, 5], dtype=torch.int32, device="cuda")
