@@ -81,6 +81,18 @@ __global__ void __launch_bounds__(GrCfg<NB, MT>::kThreads, GrCfg<NB, MT>::kCtas)
     pdl_trigger();
     const int r = p.r, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int items = p.tiles * p.count;
+    // Up to 32 adapters are taken in the order of their token counts, the longest first: the items that start last are
+    // then the shortest, and the tail of the grid is short.
+    __shared__ int s_order[32];
+    if (warp == 0 && p.count <= 32) {
+        const int c = lane < p.count ? __ldg(p.start + lane + 1) - __ldg(p.start + lane) : -1;
+        int ahead = 0;
+        for (int b = 0; b < 32; ++b) {
+            const int o = __shfl_sync(0xffffffffu, c, b);
+            ahead += o > c || (o == c && b < lane);
+        }
+        s_order[ahead] = lane;
+    }
     struct Item {  // 128 MT rows of one adapter
         int a, p0, cnt;
         bool dA;
@@ -91,6 +103,7 @@ __global__ void __launch_bounds__(GrCfg<NB, MT>::kThreads, GrCfg<NB, MT>::kCtas)
         if (i < items) {
             t.a = i / p.tiles;
             const int tile = i - t.a * p.tiles;
+            if (p.count <= 32) t.a = s_order[t.a];
             t.dA = tile >= p.tilesB;
             t.M = t.dA ? p.M[1] : p.M[0];
             t.m0 = (int64_t)(t.dA ? tile - p.tilesB : tile) * 128 * MT;

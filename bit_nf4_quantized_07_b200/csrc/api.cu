@@ -141,6 +141,7 @@ MultiWs multi_layout(bool bwd, int64_t n, int r) {
 }
 
 constexpr int64_t kMaxMultiTokens = (int64_t)1 << 24;
+constexpr int64_t kMaxStreamWeights = (int64_t)24 << 20;
 
 qln_status check_multi(const qln_nf4_weight *w, const qln_adapter_pool *pool, const uint16_t *X, int64_t n,
                        const int32_t *ids) {
@@ -478,8 +479,11 @@ qln_status qlora_multi_fwd(const qln_nf4_weight *w, const qln_adapter_pool *pool
     uint16_t *sU = reinterpret_cast<uint16_t *>(wsb + L.scaled);
     int *status = reinterpret_cast<int *>(wsb);
     cudaError_t e;
-    if (qln::nf4_decode_fwd_supported(w, n, pool->r, true)) {
-        // decode-sized n: U, then the weight stream beside it (which clears the status word)
+    // Decode-sized n: U, then the weight stream (which clears the status word).  Beyond 16 tokens its shared-memory
+    // traffic per weight makes it the slower one for large weights (11008 x 4096, 32 tokens: 51 us against the GEMM's 40;
+    // 8192 x 8192, 30: 84 against 54), while small ones still gain (4096 x 4096, 24: 20 against 30; 32: 30 against 31).
+    const bool streams = n <= 16 || w->rows * w->cols <= kMaxStreamWeights;
+    if (streams && qln::nf4_decode_fwd_supported(w, n, pool->r, true)) {
         e = qln::launch_adapter_down_small(X, n, w->cols, pool, ids, U_out, sU, cs);
         if (e != cudaSuccess) return QLN_ERR_CUDA;
         return from_cuda(qln::launch_nf4_decode_fwd_multi(w, X, n, sU, pool, ids, Y, status, cs));
