@@ -474,6 +474,10 @@ def _check_multi(w: NF4Weight, pool: AdapterPool, X, ids, others):
             raise ValueError(f"{name} must be a contiguous CUDA tensor on the pool's device")
     if index < 0:
         raise ValueError("tensors must be contiguous CUDA tensors")
+    numel, consts = w.rows * w.cols, w.absmax if w.qabs is None else w.qabs
+    if 2 * w.codes.numel() < numel or (consts is not None and 64 * consts.numel() < numel) or \
+            (w.qabs is not None and w.dq_scale is not None and 16384 * w.dq_scale.numel() < numel):
+        raise ValueError(f"the weight's codes or constants hold fewer than {w.rows} x {w.cols} weights")
     _need_current(index, w.codes, w.absmax, w.qabs, w.dq_scale, w.dq_mean)
     return index
 
@@ -566,32 +570,34 @@ class _TensorList:
         self.device = params[0].device
         self.tensors = {}
         self.count = count
-        self.array = (self._ctype * count)()
-        spans = []  # (first byte, end, written)
+        index, sizes = params[0].get_device(), [p.numel() for p in params]
+        if min(sizes) < 1:
+            raise ValueError(f"tensor {sizes.index(min(sizes))}: a parameter is empty")
+        spans = []    # (first byte, end, written)
+        columns = []  # the descriptors' pointers, field by field
         for name, (ts, dtypes, size) in fields.items():
-            if ts is None:
-                continue
-            ts = list(ts)
+            ts = [None] * count if ts is None else list(ts)
             if len(ts) != count:
                 raise ValueError(f"{len(ts)} {name} tensors for {count} parameters")
             self.tensors[name] = ts
-            for i, t in enumerate(ts):
+            column = []
+            for i, (t, n) in enumerate(zip(ts, sizes)):
                 if t is None and name == "param_bf16":
+                    column.append(None)
                     continue
-                n = params[i].numel()
-                if n < 1:
-                    raise ValueError(f"tensor {i}: a parameter is empty")
                 if t.dtype not in dtypes:
                     raise ValueError(f"tensor {i}: {name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
                 if t.numel() != size(n):
                     raise ValueError(f"tensor {i}: {name} holds {t.numel()} elements, needs {size(n)}")
                 if not t.is_contiguous():
                     raise ValueError(f"tensor {i}: {name} must be contiguous")
-                if t.device != self.device:
+                if t.get_device() != index:
                     raise ValueError(f"tensor {i}: {name} is on {t.device}, the first parameter on {self.device}")
-                setattr(self.array[i], name, t.data_ptr())
-                self.array[i].n = n
-                spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), name != "grad"))
+                at = t.data_ptr()
+                column.append(at)
+                spans.append((at, at + size(n) * t.element_size(), name != "grad"))
+            columns.append(column)
+        self.array = (self._ctype * count)(*(self._ctype(*row) for row in zip(*columns, sizes)))
         spans.sort()
         end, end_written = 0, False  # the furthest end so far, and whether a written buffer reaches it
         for a, b, written in spans:

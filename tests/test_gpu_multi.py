@@ -161,9 +161,10 @@ def test_backward(g):
     assert api.device_status(ws) == 0
 
 
-@pytest.mark.parametrize("n,cols", [(20, 4096), (48, 4096), (32, 2048), (12, 11008)])
-def test_forward_long_sums(n, cols):
-    c = Case(1024, cols, n, 9, 16, "random", True)
+@pytest.mark.parametrize("rows,cols,n", [(1024, 4096, 20), (1024, 4096, 48), (1024, 2048, 32), (1024, 11008, 12),
+                                         (4096, 8192, 20), (4096, 8192, 16), (1024, 8192, 300)])
+def test_forward_long_sums(rows, cols, n):
+    c = Case(rows, cols, n, 9, 16, "random", True)
     Y, U = c.fwd()
     Yr, Yt, Ur, Ut = c.forward_ref()
     _near("U", U, Ur, Ut)
@@ -295,6 +296,38 @@ def test_rows_behind_the_batch_stay_as_they_were():
             assert (t[n:] == 7).all() and not (t[:n] == 7).all(), n
 
 
+def test_views_into_larger_buffers():
+    """Inputs and outputs that begin inside other allocations, 16 bytes from their start; what lies around stays."""
+    c = Case(256, 512, 90, 3, 16, "random")
+    Y0, U0 = c.fwd()
+    G0 = c.bwd(U=U0)
+
+    def inside(t, fill=7.0):
+        skip = 16 // t.element_size()
+        whole = torch.full((t.numel() + 2 * skip,), fill, dtype=t.dtype, device="cuda")
+        view = whole[skip:-skip].view(t.shape)
+        view.copy_(t)
+        return whole, view, skip
+    (_, X, _), (_, dY, _), (_, ids, _) = inside(c.X), inside(c.dY), inside(c.ids, 0)
+    (_, A, _), (_, B, _) = inside(c.A), inside(c.B)
+    pool = api.AdapterPool(A, B, c.s)
+    outs = [inside(torch.zeros_like(t)) for t in (Y0, U0, *G0)]
+    api.qlora_multi_fwd(c.w, pool, X, ids, Y=outs[0][1], U_out=outs[1][1])
+    api.qlora_multi_bwd(c.w, pool, X, ids, dY, U=outs[1][1], dX=outs[2][1], dA=outs[3][1], dB=outs[4][1])
+    for (whole, view, skip), ref in zip(outs, (Y0, U0, *G0)):
+        assert torch.equal(view, ref)
+        assert (whole[:skip] == 7).all() and (whole[-skip:] == 7).all()
+
+
+def test_malformed_weights_are_refused():
+    c = Case(256, 512, 5, 2, 8, "random")
+    for bad in (dict(codes=c.w.codes[:-16]), dict(qabs=c.w.qabs[:-1]), dict(dq_scale=c.w.dq_scale[:-1])):
+        w = api.NF4Weight(**dict(dict(codes=c.w.codes, rows=256, cols=512, qabs=c.w.qabs, dq_scale=c.w.dq_scale,
+                                      dq_mean=c.w.dq_mean), **bad))
+        with pytest.raises(ValueError, match="weight"):
+            api.qlora_multi_fwd(w, c.pool, c.X, c.ids)
+
+
 def test_one_adapter_agrees_with_the_single_adapter_call():
     """With one adapter for all tokens the two entry points compute the same thing: Y and dX within two bf16 roundings
     (and the rounding of U and G to bf16), through different kernels."""
@@ -343,8 +376,11 @@ def test_adapters_train_together_and_serve():
     _near("U", U, Ur, Ut)
 
 
-def test_largest_pool():
-    c = Case(64, 64, 1500, 1024, 8, "random", True)
+@pytest.mark.parametrize("rows,cols,n,r,vary", [(64, 64, 1500, 8, True), (128, 128, 900, 24, True), (256, 512, 1100, 128, False),
+                                                (512, 1024, 290, 40, True)])
+def test_largest_pool(rows, cols, n, r, vary):
+    """Hundreds of adapters within one tile of tokens, chunks of several ranks, with and without a K split."""
+    c = Case(rows, cols, n, 1024, r, "random", vary)
     Y, U = c.fwd()
     Yr, Yt, Ur, Ut = c.forward_ref()
     _near("Y", Y, Yr, Yt)
