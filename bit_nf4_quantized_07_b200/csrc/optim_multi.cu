@@ -40,23 +40,22 @@ constexpr int kBlock8 = QLN_ADAMW8_BLOCK;
 constexpr float kE4m3Max = 448.f;
 
 // Tensors per launch: the table and its arguments stay within the 32,764
-// bytes of a launch's parameters.
-constexpr int kMtMax = 480;
+// bytes of a launch's parameters.  Short lists take a short table (the launch
+// copies all of it: 14 tensors XX us a call instead of YY).
+constexpr int kMtMax = 480, kMtFew = 48;
 struct MtArgs {
     float lr, b1, b2, eps, wd;
     const int64_t *step;
     int count;
-    uint32_t chunk0[kMtMax + 1];  // first chunk of each tensor; [count] = all chunks
 };
-struct Mt32Table {
+template <typename Tensor, int N>
+struct MtTable {
     MtArgs a;
-    qln_adamw_tensor t[kMtMax];
+    uint32_t chunk0[N + 1];  // first chunk of each tensor; [count] = all chunks
+    Tensor t[N];
 };
-struct Mt8Table {
-    MtArgs a;
-    qln_adamw8_tensor t[kMtMax];
-};
-static_assert(sizeof(Mt32Table) <= 32764 && sizeof(Mt8Table) <= 32764, "kernel parameter limit");
+static_assert(sizeof(MtTable<qln_adamw_tensor, kMtMax>) <= 32764 && sizeof(MtTable<qln_adamw8_tensor, kMtMax>) <= 32764,
+              "kernel parameter limit");
 
 // b^t by squaring (t >= 1), binary64: relative error about t 2^-53 while b^t
 // is not negligible against 1.
@@ -98,33 +97,36 @@ struct MtRange {
     uint32_t c, end;
     int ti;
 };
-__device__ __forceinline__ MtRange mt_range(const MtArgs &a) {
-    const uint64_t total = a.chunk0[a.count];
+template <typename Table>
+__device__ __forceinline__ MtRange mt_range(const Table &T) {
+    const uint64_t total = T.chunk0[T.a.count];
     MtRange r;
     r.c = (uint32_t)(total * blockIdx.x / gridDim.x);
     r.end = (uint32_t)(total * (blockIdx.x + 1) / gridDim.x);
-    int lo = 0, hi = a.count;  // chunk0[lo] <= c < chunk0[hi]
+    int lo = 0, hi = T.a.count;  // chunk0[lo] <= c < chunk0[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (a.chunk0[mid] <= r.c) lo = mid;
+        if (T.chunk0[mid] <= r.c) lo = mid;
         else hi = mid;
     }
     r.ti = lo;
     return r;
 }
 
-__global__ void __launch_bounds__(kMtThreads, kMtCtas) adamw_multi_kernel(const __grid_constant__ Mt32Table T) {
+template <int N>
+__global__ void __launch_bounds__(kMtThreads, kMtCtas)
+adamw_multi_kernel(const __grid_constant__ MtTable<qln_adamw_tensor, N> T) {
     __shared__ MtStep sh;
-    MtRange R = mt_range(T.a);
+    MtRange R = mt_range(T);
     pdl_wait();
     pdl_trigger();
     if (threadIdx.x == 0) sh = mt_step(T.a);
     __syncthreads();
     const MtStep S = sh;
     for (; R.c < R.end; ++R.c) {
-        while (R.c >= T.a.chunk0[R.ti + 1]) ++R.ti;
+        while (R.c >= T.chunk0[R.ti + 1]) ++R.ti;
         const qln_adamw_tensor &t = T.t[R.ti];
-        const int64_t e0 = (int64_t)(R.c - T.a.chunk0[R.ti]) * kMtChunk;
+        const int64_t e0 = (int64_t)(R.c - T.chunk0[R.ti]) * kMtChunk;
         const int64_t left = t.n - e0;
         if (left >= kMtChunk) {
             float4 p[2], g[2], m[2], v[2];
@@ -207,11 +209,13 @@ __device__ __forceinline__ void block_scale(uint32_t max_bits, float &inv, float
 // works on the present one's; a tensor's partial last block is read in its turn.
 constexpr int k8Ctas = 3;
 
-__global__ void __launch_bounds__(kMtThreads, k8Ctas) adamw8_multi_kernel(const __grid_constant__ Mt8Table T) {
+template <int N>
+__global__ void __launch_bounds__(kMtThreads, k8Ctas)
+adamw8_multi_kernel(const __grid_constant__ MtTable<qln_adamw8_tensor, N> T) {
     static_assert(kBlock8 == 256 && kMtChunk == 8 * kBlock8, "one block per warp and step");
     __shared__ MtStep sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    MtRange R = mt_range(T.a);
+    MtRange R = mt_range(T);
     pdl_wait();
     pdl_trigger();
     struct Raw {  // this lane's 8 elements of a whole block
@@ -224,9 +228,9 @@ __global__ void __launch_bounds__(kMtThreads, k8Ctas) adamw8_multi_kernel(const 
     int ati = R.ti;
     auto request = [&]() {
         if (ac < R.end) {
-            while (ac >= T.a.chunk0[ati + 1]) ++ati;
+            while (ac >= T.chunk0[ati + 1]) ++ati;
             const qln_adamw8_tensor &t = T.t[ati];
-            const int64_t blk = (int64_t)(ac - T.a.chunk0[ati]) * (kMtChunk / kBlock8) + warp;
+            const int64_t blk = (int64_t)(ac - T.chunk0[ati]) * (kMtChunk / kBlock8) + warp;
             if ((blk + 1) * kBlock8 <= t.n) {
                 const int64_t e = blk * kBlock8 + 8 * lane;
 #pragma unroll
@@ -250,9 +254,9 @@ __global__ void __launch_bounds__(kMtThreads, k8Ctas) adamw8_multi_kernel(const 
     for (; R.c < R.end; ++R.c) {
         const Raw cur = nxt;
         request();
-        while (R.c >= T.a.chunk0[R.ti + 1]) ++R.ti;
+        while (R.c >= T.chunk0[R.ti + 1]) ++R.ti;
         const qln_adamw8_tensor &t = T.t[R.ti];
-        const int64_t blk = (int64_t)(R.c - T.a.chunk0[R.ti]) * (kMtChunk / kBlock8) + warp;
+        const int64_t blk = (int64_t)(R.c - T.chunk0[R.ti]) * (kMtChunk / kBlock8) + warp;
         const int64_t e = blk * kBlock8 + 8 * lane;  // this lane's 8 elements
         if (blk * kBlock8 >= t.n) continue;
         const bool whole = (blk + 1) * kBlock8 <= t.n;
@@ -361,32 +365,43 @@ static cudaError_t page_tensor(const qln_adamw8_tensor &t, bool in, int dev, cud
     return page_managed(t.v_scale, s, dev, st);
 }
 
-template <typename Table, typename Tensor>
-static cudaError_t launch_multi(void (*kernel)(const Table), int ctas, const Tensor *tensors, int count,
-                                const qln_adamw_config *cfg, const int64_t *step, int flags, cudaStream_t st, int num_sms) {
+// The update itself, N tensors at a time at most.
+template <typename Tensor, int N>
+static cudaError_t launch_tables(void (*kernel)(const MtTable<Tensor, N>), int ctas, const Tensor *tensors, int count,
+                                 const MtArgs &args, cudaStream_t st, int num_sms) {
+    MtTable<Tensor, N> T;
+    T.a = args;
+    for (int i0 = 0; i0 < count; i0 += T.a.count) {
+        const int k = count - i0 < N ? count - i0 : N;
+        uint64_t chunks = 0;
+        T.a.count = k;
+        for (int i = 0; i < k; ++i) {
+            T.chunk0[i] = (uint32_t)chunks;
+            T.t[i] = tensors[i0 + i];
+            chunks += (uint64_t)(tensors[i0 + i].n + kMtChunk - 1) / kMtChunk;
+        }
+        T.chunk0[k] = (uint32_t)chunks;
+        const uint64_t wave = (uint64_t)num_sms * ctas;
+        const cudaError_t e = launch_pdl(kernel, dim3((unsigned)(chunks < wave ? chunks : wave)), dim3(kMtThreads), 0, st, T);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+template <typename Tensor>
+static cudaError_t launch_multi(void (*few)(const MtTable<Tensor, kMtFew>), void (*many)(const MtTable<Tensor, kMtMax>),
+                                int ctas, const Tensor *tensors, int count, const qln_adamw_config *cfg,
+                                const int64_t *step, int flags, cudaStream_t st, int num_sms) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (flags & QLN_ADAMW_PAGE_IN)
         for (int i = 0; i < count; ++i)
             if ((e = page_tensor(tensors[i], true, dev, st)) != cudaSuccess) return e;
-    Table T;
-    T.a.lr = cfg->lr, T.a.b1 = cfg->beta1, T.a.b2 = cfg->beta2, T.a.eps = cfg->eps, T.a.wd = cfg->weight_decay;
-    T.a.step = step;
-    for (int i0 = 0; i0 < count; i0 += T.a.count) {
-        const int k = count - i0 < kMtMax ? count - i0 : kMtMax;
-        uint64_t chunks = 0;
-        T.a.count = k;
-        for (int i = 0; i < k; ++i) {
-            T.a.chunk0[i] = (uint32_t)chunks;
-            T.t[i] = tensors[i0 + i];
-            chunks += (uint64_t)(tensors[i0 + i].n + kMtChunk - 1) / kMtChunk;
-        }
-        T.a.chunk0[k] = (uint32_t)chunks;
-        const uint64_t wave = (uint64_t)num_sms * ctas;
-        e = launch_pdl(kernel, dim3((unsigned)(chunks < wave ? chunks : wave)), dim3(kMtThreads), 0, st, T);
-        if (e != cudaSuccess) return e;
-    }
+    const MtArgs a{cfg->lr, cfg->beta1, cfg->beta2, cfg->eps, cfg->weight_decay, step, 0};
+    e = count <= kMtFew ? launch_tables(few, ctas, tensors, count, a, st, num_sms)
+                        : launch_tables(many, ctas, tensors, count, a, st, num_sms);
+    if (e != cudaSuccess) return e;
     if (flags & QLN_ADAMW_PAGE_OUT)
         for (int i = 0; i < count; ++i)
             if ((e = page_tensor(tensors[i], false, cudaCpuDeviceId, st)) != cudaSuccess) return e;
@@ -395,11 +410,11 @@ static cudaError_t launch_multi(void (*kernel)(const Table), int ctas, const Ten
 
 cudaError_t launch_adamw_multi(const qln_adamw_tensor *t, int count, const qln_adamw_config *cfg, const int64_t *step,
                                int flags, cudaStream_t st, int num_sms) {
-    return launch_multi<Mt32Table>(adamw_multi_kernel, kMtCtas, t, count, cfg, step, flags, st, num_sms);
+    return launch_multi<qln_adamw_tensor>(adamw_multi_kernel<kMtFew>, adamw_multi_kernel<kMtMax>, kMtCtas, t, count, cfg, step, flags, st, num_sms);
 }
 cudaError_t launch_adamw8_multi(const qln_adamw8_tensor *t, int count, const qln_adamw_config *cfg, const int64_t *step,
                                 int flags, cudaStream_t st, int num_sms) {
-    return launch_multi<Mt8Table>(adamw8_multi_kernel, k8Ctas, t, count, cfg, step, flags, st, num_sms);
+    return launch_multi<qln_adamw8_tensor>(adamw8_multi_kernel<kMtFew>, adamw8_multi_kernel<kMtMax>, k8Ctas, t, count, cfg, step, flags, st, num_sms);
 }
 
 }  // namespace qln
