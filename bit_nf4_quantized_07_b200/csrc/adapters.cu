@@ -357,6 +357,7 @@ struct SmallArgs {
     const float *scale;
     float *full;       // [n][r] or null
     uint16_t *scaled;  // [n][r]
+    int *status;       // cleared: this is the first kernel of its call
 };
 
 template <int NT>  // n <= 8 NT
@@ -366,6 +367,7 @@ __global__ void __launch_bounds__(128) adapter_down_small_kernel(const SmallArgs
     pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, part = blockIdx.z;
+    if (tid == 0 && blockIdx.x == 0 && blockIdx.y == 0 && part == 0) *p.status = QLN_OK;
     const int g = lane >> 2, c = lane & 3, n = p.n, r = p.r;
     const int id = lane < n ? __ldg(p.ids + lane) : -1;
     const bool in = (unsigned)id < (unsigned)p.count;
@@ -537,8 +539,8 @@ cudaError_t launch_adapter_down(const uint16_t *in, int64_t n, int64_t K, const 
 }
 
 cudaError_t launch_adapter_down_small(const uint16_t *in, int64_t n, int64_t K, const qln_adapter_pool *pool,
-                                      const int32_t *ids, float *full, uint16_t *scaled, cudaStream_t st) {
-    const SmallArgs a{in, pool->A, (int)n, pool->r, pool->count, K, ids, pool->rank, pool->scale, full, scaled};
+                                      const int32_t *ids, float *full, uint16_t *scaled, int *status, cudaStream_t st) {
+    const SmallArgs a{in, pool->A, (int)n, pool->r, pool->count, K, ids, pool->rank, pool->scale, full, scaled, status};
     const dim3 grid((unsigned)(n < pool->count ? n : pool->count), (unsigned)((pool->r + 15) / 16), kAdCluster);
     const dim3 cl(1, 1, kAdCluster);
     switch ((n + 7) / 8) {

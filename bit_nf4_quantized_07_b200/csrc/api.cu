@@ -479,14 +479,17 @@ qln_status qlora_multi_fwd(const qln_nf4_weight *w, const qln_adapter_pool *pool
     uint16_t *sU = reinterpret_cast<uint16_t *>(wsb + L.scaled);
     int *status = reinterpret_cast<int *>(wsb);
     cudaError_t e;
-    // Decode-sized n: U, then the weight stream (which clears the status word).  Beyond 16 tokens its shared-memory
-    // traffic per weight makes it the slower one for large weights (11008 x 4096, 32 tokens: 51 us against the GEMM's 40;
-    // 8192 x 8192, 30: 84 against 54), while small ones still gain (4096 x 4096, 24: 20 against 30; 32: 30 against 31).
-    const bool streams = n <= 16 || w->rows * w->cols <= kMaxStreamWeights;
-    if (streams && qln::nf4_decode_fwd_supported(w, n, pool->r, true)) {
-        e = qln::launch_adapter_down_small(X, n, w->cols, pool, ids, U_out, sU, cs);
+    if (n <= 32) {  // one warp holds all ids: no plan
+        e = qln::launch_adapter_down_small(X, n, w->cols, pool, ids, U_out, sU, status, cs);
         if (e != cudaSuccess) return QLN_ERR_CUDA;
-        return from_cuda(qln::launch_nf4_decode_fwd_multi(w, X, n, sU, pool, ids, Y, status, cs));
+        // The weight stream, whose shared-memory and instruction cost per weight grows with every 8 tokens, or the
+        // GEMM with its K split, about 17 us and 0.42 us per million weights whatever n.  Measured (us, stream / GEMM),
+        // rank 16 to 64: 4096 x 4096 n = 8: 14 / 24, 16: 17 / 24, 24: 20 / 25, 32: 30 / 27; 8192 x 8192 n = 8: 32 / 44,
+        // 16: 50 / 45, 30: 84 / 46; 4096 x 11008 n = 12: 40 / 35, 24: 57 / 40; 11008 x 4096 n = 16: 30 / 32.
+        const bool streams = n <= 8 || (n <= 24 && w->rows * w->cols <= kMaxStreamWeights);
+        if (streams && qln::nf4_decode_fwd_supported(w, n, pool->r, true))
+            return from_cuda(qln::launch_nf4_decode_fwd_multi(w, X, n, sU, pool, ids, Y, status, cs));
+        return from_cuda(multi_gemm(w, false, X, n, sU, pool->B, pool, ids, Y, status, cs, sms));
     }
     e = qln::launch_adapter_plan(ids, n, pool->count, plan, status, cs);
     if (e != cudaSuccess) return QLN_ERR_CUDA;

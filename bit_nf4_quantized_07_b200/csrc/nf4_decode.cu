@@ -803,7 +803,7 @@ static cudaError_t launch_df(DfParams p, const qln_nf4_weight *w, cudaStream_t s
         DfLayout L;
         if (!df_plan_s(T, KB, p.r, NT, S, Q, MULTI, L)) continue;
         // blocks per CTA; with MULTI also 50 for every epoch after the first, about what its barriers and refills
-        // cost (4096 x 11008, n = 12: one epoch on clusters of 8 takes XX us, four on clusters of 4 take 67 us)
+        // cost (4096 x 11008, n = 12: one epoch on clusters of 8 takes 28 us, several on clusters of 4 take 67 us)
         const int64_t m = (T + Q - 1) / Q;
         const int64_t cost = m * L.nkb_max + (MULTI ? 50 * ((m + L.E - 1) / L.E - 1) : 0);
         if (best_cost < 0 || cost < best_cost) {

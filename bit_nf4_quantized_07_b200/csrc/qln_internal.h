@@ -115,7 +115,7 @@ cudaError_t launch_adapter_down(const uint16_t *in, int64_t n, int64_t K, const 
                                 uint16_t *aux_split, cudaStream_t st);
 // the same for n <= 32 without a plan, A only (full may be null; columns past a rank are zero in both)
 cudaError_t launch_adapter_down_small(const uint16_t *in, int64_t n, int64_t K, const qln_adapter_pool *pool,
-                                      const int32_t *ids, float *full, uint16_t *scaled, cudaStream_t st);
+                                      const int32_t *ids, float *full, uint16_t *scaled, int *status, cudaStream_t st);
 // adapter_grads.cu: dA and dB of every adapter; U3, G3: three bf16 planes of n * r
 cudaError_t launch_adapter_grads(const uint16_t *dY, const uint16_t *U3, int64_t dout, const uint16_t *X,
                                  const uint16_t *G3, int64_t din, int64_t n, const qln_adapter_pool *pool,
