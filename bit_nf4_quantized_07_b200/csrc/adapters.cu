@@ -342,12 +342,15 @@ __global__ void __launch_bounds__(128) adapter_down_kernel(const DownArgs p) {
 // ===========================================================================
 // Down product of a decode-sized batch (n <= 32), without a plan: every cluster
 // groups the ids by itself (one warp holds them all) and takes the x-th adapter
-// present and 16 of its columns; its 8 CTAs x 4 warps take the 64-blocks of K in
+// present and 16 of its columns; its CTAs x 4 warps take the 64-blocks of K in
 // turn, factor rows and tokens straight from global memory into MMA fragments
 // (A operand: 16 factor rows; B operand: 8 tokens; both with the same
 // permutation of k within a block, so each load is 16 bytes).  Latency-bound: a
 // warp has all loads of two blocks in flight, and partial sums meet in shared
-// memory, first of the warps, then of the CTAs, in a fixed order.
+// memory, first of the warps, then of the CTAs, in a fixed order.  The warps add
+// theirs one after the other into one tile: with under 4.5 KB a CTA fits beside
+// a CTA of the GEMM, which then need not wait for this kernel to start its
+// weight steps (clusters of 4 keep it to one CTA per SM).
 // ===========================================================================
 struct SmallArgs {
     const uint16_t *in, *A;
@@ -360,10 +363,11 @@ struct SmallArgs {
     int *status;       // cleared: this is the first kernel of its call
 };
 
-template <int NT>  // n <= 8 NT
+template <int NT, int CL>  // n <= 8 NT; CTAs of a cluster
 __global__ void __launch_bounds__(128) adapter_down_small_kernel(const SmallArgs p) {
-    constexpr int LD = 8 * NT + 2;
-    __shared__ float s_part[4][16][LD], s_sum[16][LD];
+    constexpr int LD = 8 * NT + 2, kCols = 16 / CL;  // columns that a CTA finishes
+    __shared__ float s_sum[16][LD];
+    __shared__ int8_t s_tok[4][32];  // per warp: the adapter's tokens
     pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, part = blockIdx.z;
@@ -371,24 +375,29 @@ __global__ void __launch_bounds__(128) adapter_down_small_kernel(const SmallArgs
     const int g = lane >> 2, c = lane & 3, n = p.n, r = p.r;
     const int id = lane < n ? __ldg(p.ids + lane) : -1;
     const bool in = (unsigned)id < (unsigned)p.count;
-    const uint32_t with = __ballot_sync(0xffffffffu, in);
+    const uint32_t with = __ballot_sync(0xffffffffu, in), below = (1u << lane) - 1u;
     const uint32_t same = __match_any_sync(0xffffffffu, in ? id : -1) & with;
-    const uint32_t leads = __ballot_sync(0xffffffffu, in && (same & ((1u << lane) - 1u)) == 0);
+    const bool first = in && (same & below) == 0;
+    const uint32_t leads = __ballot_sync(0xffffffffu, first);
     const int j0 = 16 * blockIdx.y;
-    if (p.full && blockIdx.x == 0 && warp == 0 && lane < n && !in)  // tokens without an adapter: two columns per CTA
-        for (int j = j0 + 2 * part; j < min(r, j0 + 2 * part + 2); ++j) p.full[lane * r + j] = 0.f;
-    if ((int)blockIdx.x >= __popc(leads)) return;  // the whole cluster
-    const int lead = __fns(leads, 0, blockIdx.x + 1);
+    if (p.full && blockIdx.x == 0 && warp == 0 && lane < n && !in)  // tokens without an adapter
+        for (int j = j0 + kCols * part; j < min(r, j0 + kCols * (part + 1)); ++j) p.full[lane * r + j] = 0.f;
+    const uint32_t mine = __ballot_sync(0xffffffffu, first && __popc(leads & below) == (int)blockIdx.x);
+    if (!mine) return;  // the whole cluster
+    const int lead = __ffs(mine) - 1;
     const int a = __shfl_sync(0xffffffffu, id, lead);
     const uint32_t mask = __shfl_sync(0xffffffffu, same, lead);  // its tokens
+    if ((mask >> lane) & 1u) s_tok[warp][__popc(mask & below)] = (int8_t)lane;
+    __syncwarp();
+    const int8_t *tok = s_tok[warp];
     const int rk = adapter_rank(p.rank, a, r), cnt = __popc(mask);
     if (j0 >= rk) {  // zero past the rank
         if (part == 0)
             for (int i = tid; i < 16 * cnt; i += 128) {
-                const int t = __fns(mask, 0, i / 16 + 1), j = j0 + i % 16;
-                if (j >= r) continue;
-                p.scaled[t * r + j] = 0;
-                if (p.full) p.full[t * r + j] = 0.f;
+                const int at = tok[i / 16] * r + j0 + i % 16;
+                if (j0 + i % 16 >= r) continue;
+                p.scaled[at] = 0;
+                if (p.full) p.full[at] = 0.f;
             }
         return;
     }
@@ -397,7 +406,7 @@ __global__ void __launch_bounds__(128) adapter_down_small_kernel(const SmallArgs
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         xok[nt] = 8 * nt + g < cnt;
-        xr[nt] = p.in + (xok[nt] ? (int64_t)__fns(mask, 0, 8 * nt + g + 1) * p.K : 0) + 16 * c;
+        xr[nt] = p.in + (xok[nt] ? (int64_t)tok[8 * nt + g] * p.K : 0) + 16 * c;
     }
     const bool ok0 = j0 + g < r, ok1 = j0 + g + 8 < r;
     const uint16_t *f0 = p.A + ((int64_t)a * r + (ok0 ? j0 + g : 0)) * p.K + 16 * c;
@@ -410,7 +419,7 @@ __global__ void __launch_bounds__(128) adapter_down_small_kernel(const SmallArgs
         for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
     const int KB = (int)(p.K / 64);
 #pragma unroll 2
-    for (int b = part * 4 + warp; b < KB; b += 32) {
+    for (int b = part * 4 + warp; b < KB; b += 4 * CL) {
         const int64_t o = (int64_t)b * 64;
         uint4 fa[4], xa[NT][2];
 #pragma unroll
@@ -432,30 +441,35 @@ __global__ void __launch_bounds__(128) adapter_down_small_kernel(const SmallArgs
             }
         }
     }
+#pragma unroll 1
+    for (int w = 0; w < 4; ++w) {  // the warps' sums, in their order
+        if (warp == w) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<float2 *>(&s_part[warp][g + 8 * h][8 * nt + 2 * c]) = make_float2(acc[nt][2 * h], acc[nt][2 * h + 1]);
-    __syncthreads();
-    for (int i = tid; i < 16 * cnt; i += 128) {
-        const int j = i % 16, k = i / 16;
-        s_sum[j][k] = __fadd_rn(__fadd_rn(__fadd_rn(s_part[0][j][k], s_part[1][j][k]), s_part[2][j][k]), s_part[3][j][k]);
+                for (int h = 0; h < 2; ++h) {
+                    float2 *at = reinterpret_cast<float2 *>(&s_sum[g + 8 * h][8 * nt + 2 * c]);
+                    float2 v = w ? *at : make_float2(0.f, 0.f);
+                    v.x = __fadd_rn(v.x, acc[nt][2 * h]);
+                    v.y = __fadd_rn(v.y, acc[nt][2 * h + 1]);
+                    *at = v;
+                }
+        }
+        __syncthreads();
     }
-    __syncwarp();
     ad_cluster_sync();
     const float s = __ldg(p.scale + a);
     const uint32_t base = smem_u32(&s_sum[0][0]);
-    for (int i = tid; i < 2 * cnt; i += 128) {  // two columns per CTA
-        const int j = 2 * part + (i & 1), k = i >> 1;
-        float x[kAdCluster], v = 0.f;
+    for (int i = tid; i < kCols * cnt; i += 128) {
+        const int j = kCols * part + i % kCols, k = i / kCols;
+        float x[CL], v = 0.f;
 #pragma unroll
-        for (int q = 0; q < kAdCluster; ++q) x[q] = ad_peer_f32(base + (uint32_t)(j * LD + k) * 4u, q);
+        for (int q = 0; q < CL; ++q) x[q] = ad_peer_f32(base + (uint32_t)(j * LD + k) * 4u, q);
 #pragma unroll
-        for (int q = 0; q < kAdCluster; ++q) v = __fadd_rn(v, x[q]);
+        for (int q = 0; q < CL; ++q) v = __fadd_rn(v, x[q]);
         if (j0 + j >= r) continue;
         if (j0 + j >= rk) v = 0.f;
-        const int at = __fns(mask, 0, k + 1) * r + j0 + j;
+        const int at = tok[k] * r + j0 + j;
         if (p.full) p.full[at] = v;
         p.scaled[at] = __bfloat16_as_ushort(__float2bfloat16_rn(__fmul_rn(s, v)));
     }
@@ -541,14 +555,18 @@ cudaError_t launch_adapter_down(const uint16_t *in, int64_t n, int64_t K, const 
 cudaError_t launch_adapter_down_small(const uint16_t *in, int64_t n, int64_t K, const qln_adapter_pool *pool,
                                       const int32_t *ids, float *full, uint16_t *scaled, int *status, cudaStream_t st) {
     const SmallArgs a{in, pool->A, (int)n, pool->r, pool->count, K, ids, pool->rank, pool->scale, full, scaled, status};
-    const dim3 grid((unsigned)(n < pool->count ? n : pool->count), (unsigned)((pool->r + 15) / 16), kAdCluster);
-    const dim3 cl(1, 1, kAdCluster);
+    const unsigned groups = (unsigned)(n < pool->count ? n : pool->count), jt = (unsigned)((pool->r + 15) / 16);
+    // Clusters of 8 for the shortest chain; of 4 where those would put two CTAs on an SM.
+#define QLN_AD_SMALL(NT) \
+    (groups * jt * 8 <= 148 ? launch_cluster(adapter_down_small_kernel<NT, 8>, dim3(groups, jt, 8), dim3(1, 1, 8), 0, st, a) \
+                            : launch_cluster(adapter_down_small_kernel<NT, 4>, dim3(groups, jt, 4), dim3(1, 1, 4), 0, st, a))
     switch ((n + 7) / 8) {
-        case 1: return launch_cluster(adapter_down_small_kernel<1>, grid, cl, 0, st, a);
-        case 2: return launch_cluster(adapter_down_small_kernel<2>, grid, cl, 0, st, a);
-        case 3: return launch_cluster(adapter_down_small_kernel<3>, grid, cl, 0, st, a);
-        default: return launch_cluster(adapter_down_small_kernel<4>, grid, cl, 0, st, a);
+        case 1: return QLN_AD_SMALL(1);
+        case 2: return QLN_AD_SMALL(2);
+        case 3: return QLN_AD_SMALL(3);
+        default: return QLN_AD_SMALL(4);
     }
+#undef QLN_AD_SMALL
 }
 
 }  // namespace qln
