@@ -153,11 +153,13 @@ __device__ __forceinline__ void split3(float v, uint16_t (&q)[3]) {
 
 // ===========================================================================
 // Down product: v[t][j] = sum_k in[t][k] f_a(j, k), f_a = A_a [r][K] (WKM =
-// false) or B_a [K][r] (WKM = true).  A cluster of 8 CTAs owns a tile of up to
-// 64 tokens of one adapter (gathered rows) x all r columns; each CTA takes an
-// eighth of K, streamed through a 4-stage cp.async ring, 4 warps x 16 tokens;
-// the eight partial tiles meet in shared memory and are added in the order of
-// the CTAs, each CTA finishing 8 tokens.  HBM-bound: the activations are read
+// false) or B_a [K][r] (WKM = true).  A cluster of 8 or 4 CTAs owns a tile of up
+// to 64 tokens of one adapter (gathered rows) x all r columns; each CTA takes
+// its share of K, streamed through a 4-stage cp.async ring, 4 warps x 16 tokens;
+// the partial tiles meet in shared memory and are added in the order of the
+// CTAs, each CTA finishing its share of the tokens.  HBM-bound for small ranks
+// (at rank 64 a tile reads as much of the factor, from L2, as of the tokens:
+// 5 TB/s of loads together): the activations are read
 // once, each adapter once per tile, and nothing is written but the result.
 // The tensor cores' running sums move into fp32 registers every 8 chunks of 64
 // (their additions truncate, and the error would grow with K).
@@ -167,7 +169,7 @@ __device__ __forceinline__ void split3(float v, uint16_t (&q)[3]) {
 // adapter get zeros in full only (nothing else of them is read).  With `aux`,
 // its rows (an fp32 [n][r]) are split into aux_split along the way.
 // ===========================================================================
-constexpr int kAdStages = 4, kAdFlush = 8, kAdCluster = 8;
+constexpr int kAdStages = 4, kAdFlush = 8, kAdCluster = 8;  // kAdCluster: at most
 constexpr int kAdLd = 72;  // padded row (bf16) of the staged tiles
 
 struct DownArgs {
@@ -197,16 +199,17 @@ __global__ void __launch_bounds__(128) adapter_down_kernel(const DownArgs p) {
     const int p0 = __ldg(p.start + a) + 64 * (tile - __ldg(p.tiles + a));
     const int rows = min(64, __ldg(p.start + a + 1) - p0);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, part = blockIdx.y;
-    if (a == count) {  // tokens without an adapter: an eighth of the rows per CTA
+    const int cl = gridDim.y, own = 64 / cl;  // CTAs of the cluster, rows that each finishes
+    if (a == count) {  // tokens without an adapter
         if (p.full)
-            for (int i = tid; i < 8 * r; i += 128)
-                if (8 * part + i / r < rows) p.full[(int64_t)__ldg(p.order + p0 + 8 * part + i / r) * r + i % r] = 0.f;
+            for (int i = tid; i < own * r; i += 128)
+                if (own * part + i / r < rows) p.full[(int64_t)__ldg(p.order + p0 + own * part + i / r) * r + i % r] = 0.f;
         return;
     }
     const uint16_t *wt = p.pool + (int64_t)a * r * K;
     const int g = lane >> 2, c = lane & 3;
     const int nch = (int)(K / 64);
-    const int ch0 = nch * part / kAdCluster, ch1 = nch * (part + 1) / kAdCluster;
+    const int ch0 = nch * part / cl, ch1 = nch * (part + 1) / cl;
 
     const uint16_t *src[4];  // this thread's four token rows of a stage (null: a row past the tile)
 #pragma unroll
@@ -311,14 +314,15 @@ __global__ void __launch_bounds__(128) adapter_down_kernel(const DownArgs p) {
     const float s = __ldg(p.scale + a);
     const uint32_t base = smem_u32(part_s);
     const int64_t plane = n * r;
-    for (int i = tid; i < 8 * r; i += 128) {  // 8 tokens x r columns per CTA
-        const int row = 8 * part + i / r, j = i % r;
+    for (int i = tid; i < own * r; i += 128) {
+        const int row = own * part + i / r, j = i % r;
         if (row >= rows) break;
         float x[kAdCluster], v = 0.f;
 #pragma unroll
-        for (int q = 0; q < kAdCluster; ++q) x[q] = ad_peer_f32(base + (uint32_t)(row * PLD + j) * 4u, q);
+        for (int q = 0; q < kAdCluster; ++q) x[q] = q < cl ? ad_peer_f32(base + (uint32_t)(row * PLD + j) * 4u, q) : 0.f;
 #pragma unroll
-        for (int q = 0; q < kAdCluster; ++q) v = __fadd_rn(v, x[q]);
+        for (int q = 0; q < kAdCluster; ++q)
+            if (q < cl) v = __fadd_rn(v, x[q]);
         if (j >= rk) v = 0.f;
         const int64_t at = (int64_t)__ldg(p.order + p0 + row) * r + j;
         if (p.full) p.full[at] = v;
@@ -535,7 +539,10 @@ static cudaError_t launch_ad_down(const DownArgs &a, cudaStream_t st) {
     static_assert(smem >= 64 * (NT * 8 + 4) * 4, "the partial tile fits into the ring");
     // every group's last tile may be partial: at most n / 64 whole tiles and one more per group present
     const int64_t tiles = a.n / 64 + (a.count + 1 < a.n ? a.count + 1 : a.n);
-    return launch_cluster(adapter_down_kernel<NT, WKM>, dim3((unsigned)tiles, kAdCluster), dim3(1, kAdCluster), smem, st, a);
+    // Eight CTAs per tile while all fit at once, else four (28672 columns, rank 64, 4096 tokens: 99 us against 115).
+    const int64_t slots = 148 * ((int64_t)(228 * 1024) / (int64_t)(smem + 1024));
+    const unsigned cl = tiles * kAdCluster <= slots ? kAdCluster : kAdCluster / 2;
+    return launch_cluster(adapter_down_kernel<NT, WKM>, dim3((unsigned)tiles, cl), dim3(1, cl), smem, st, a);
 }
 
 cudaError_t launch_adapter_down(const uint16_t *in, int64_t n, int64_t K, const qln_adapter_pool *pool, bool kmajor,
