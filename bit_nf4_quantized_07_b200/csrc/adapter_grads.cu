@@ -8,8 +8,8 @@
 //
 // HBM-bound (P is read once, Q is narrow), so everything else has to stay out
 // of the way of the loads.  An item is 128 MT rows m of one adapter over all of
-// its tokens, K in steps of 64 gathered tokens; a CTA works through every
-// gridDim.x-th item without draining its ring in between.  Producer warps copy
+// its tokens, K in steps of 64 gathered tokens; a CTA works through its share of
+// the items without draining its ring in between.  Producer warps copy
 // the token rows by cp.async into swizzled tiles (a row of P or Q is one K of an
 // MN-major operand, so nothing is transposed), their token numbers read two
 // steps ahead; one thread issues the MMAs; 4 MT warps add up and store.  Q
@@ -81,8 +81,8 @@ __global__ void __launch_bounds__(GrCfg<NB, MT>::kThreads, GrCfg<NB, MT>::kCtas)
     pdl_trigger();
     const int r = p.r, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int items = p.tiles * p.count;
-    // Up to 32 adapters are taken in the order of their token counts, the longest first: the items that start last are
-    // then the shortest, and the tail of the grid is short.
+    // Up to 32 adapters are taken in the order of their token counts, the longest first: the last round's items are then
+    // the shortest, and the tail of the grid is short.
     __shared__ int s_order[32];
     if (warp == 0 && p.count <= 32) {
         const int c = lane < p.count ? __ldg(p.start + lane + 1) - __ldg(p.start + lane) : -1;
@@ -112,6 +112,9 @@ __global__ void __launch_bounds__(GrCfg<NB, MT>::kThreads, GrCfg<NB, MT>::kCtas)
         }
         return t;
     };
+    const int G = (int)gridDim.x, cta = (int)blockIdx.x;
+    // This CTA's k-th item (past the last: none).  Every other round runs backwards, so that a CTA gets long and short ones.
+    auto nth = [&](int k) { return k * G + (k & 1 ? G - 1 - cta : cta); };
     auto steps_of = [](const Item &t) { return (t.cnt + kGrBK - 1) / kGrBK; };
 
     if (tid == 0) {
@@ -152,14 +155,14 @@ __global__ void __launch_bounds__(GrCfg<NB, MT>::kThreads, GrCfg<NB, MT>::kCtas)
             bool in0, in1;  // the chunk's columns of the two sub-tiles exist
             bool live;
         };
-        int next_item = blockIdx.x, st = 0, left = 0;  // the look-ahead: its item's next step, steps left
-        Item it = item_at(next_item), nx = item_at(next_item + gridDim.x);
+        int rnd = 0, st = 0, left = 0;  // the look-ahead: its item's next step, steps left
+        Item it = item_at(nth(0)), nx = item_at(nth(1));
         left = steps_of(it);
         auto look = [&](Step &x) {
-            while (left == 0 && next_item < items) {
-                next_item += gridDim.x;
+            while (left == 0 && rnd * G < items) {
+                ++rnd;
                 it = nx;
-                nx = item_at(next_item + gridDim.x);
+                nx = item_at(nth(rnd + 1));
                 left = steps_of(it);
                 st = 0;
             }
@@ -235,10 +238,10 @@ __global__ void __launch_bounds__(GrCfg<NB, MT>::kThreads, GrCfg<NB, MT>::kCtas)
             const uint32_t idesc = tc::idesc_bf16_f32(128, NB, true, true);
             int k = 0, grp = 0;  // steps and groups so far
             bool ok = true;
-            Item nx = item_at(blockIdx.x);
-            for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
+            Item nx = item_at(nth(0));
+            for (int rnd = 0; ok && rnd * G < items; ++rnd) {
                 const int steps = steps_of(nx);
-                nx = item_at(i + gridDim.x);
+                nx = item_at(nth(rnd + 1));
                 for (int st = 0; st < steps; ++st, ++k) {
                     const int s = k % S, b = grp & 1;
                     const bool first = st % kGrGroup == 0, last = st % kGrGroup == kGrGroup - 1 || st == steps - 1;
@@ -274,10 +277,10 @@ __global__ void __launch_bounds__(GrCfg<NB, MT>::kThreads, GrCfg<NB, MT>::kCtas)
         const int mt = warp >> 2, quad = warp & 3;
         int grp = 0;
         bool ok = true;
-        Item nx = item_at(blockIdx.x);
-        for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
+        Item nx = item_at(nth(0));
+        for (int rnd = 0; ok && rnd * G < items; ++rnd) {
             const Item t = nx;
-            nx = item_at(i + gridDim.x);
+            nx = item_at(nth(rnd + 1));
             float sum[NB];
 #pragma unroll
             for (int j = 0; j < NB; ++j) sum[j] = 0.f;
@@ -348,11 +351,11 @@ static cudaError_t launch_grad(GradArgs &a, cudaStream_t st, int num_sms) {
     if (e != cudaSuccess) return e;
     a.tilesB = (int)((a.M[0] + 128 * MT - 1) / (128 * MT));
     a.tiles = a.tilesB + (int)((a.M[1] + 128 * MT - 1) / (128 * MT));
-    // One wave that walks the items where each CTA gets many, so that their lengths even out (28672 x 8192, 8 adapters of
-    // about 512 tokens: 120 us against 168); otherwise a CTA per item, placed as SMs come free (11008 x 4096, 4 adapters
-    // of 100 to 1100 tokens: 31 us against 42).
+    // One wave that walks the items: their rings do not drain in between, and no CTA starts late.  A CTA per item instead
+    // (whole calls, us): 4096 x 4096, 100 tokens of 8 adapters 37.4 / 35.1; 1000 tokens of 40 adapters, rank 32: 161 / 144;
+    // 4096 x 11008, 2048 tokens of 16 adapters, rank 64: 265 / 242.
     const int64_t items = (int64_t)a.tiles * a.count, wave = (int64_t)num_sms * C::kCtas;
-    return launch_pdl(kern, dim3((unsigned)(items < 4 * wave ? items : wave)), dim3(C::kThreads), (size_t)C::kSmem, st, a);
+    return launch_pdl(kern, dim3((unsigned)(items < wave ? items : wave)), dim3(C::kThreads), (size_t)C::kSmem, st, a);
 }
 
 cudaError_t launch_adapter_grads(const uint16_t *dY, const uint16_t *U3, int64_t dout, const uint16_t *X,
