@@ -326,7 +326,8 @@ __global__ void __launch_bounds__(128) adapter_down_kernel(const DownArgs p) {
         if (j >= rk) v = 0.f;
         const int64_t at = (int64_t)__ldg(p.order + p0 + row) * r + j;
         if (p.full) p.full[at] = v;
-        if (p.scaled) p.scaled[at] = __bfloat16_as_ushort(__float2bfloat16_rn(__fmul_rn(s, v)));
+        if (p.scaled)  // (past the rank a zero, whatever the scale)
+            p.scaled[at] = __bfloat16_as_ushort(__float2bfloat16_rn(j < rk ? __fmul_rn(s, v) : 0.f));
         uint16_t q3[3];
         if (p.split) {
             split3(v, q3);
@@ -472,10 +473,10 @@ __global__ void __launch_bounds__(128) adapter_down_small_kernel(const SmallArgs
 #pragma unroll
         for (int q = 0; q < CL; ++q) v = __fadd_rn(v, x[q]);
         if (j0 + j >= r) continue;
-        if (j0 + j >= rk) v = 0.f;
+        const bool in_rank = j0 + j < rk;  // past it zeros, whatever the scale
         const int at = tok[k] * r + j0 + j;
-        if (p.full) p.full[at] = v;
-        p.scaled[at] = __bfloat16_as_ushort(__float2bfloat16_rn(__fmul_rn(s, v)));
+        if (p.full) p.full[at] = in_rank ? v : 0.f;
+        p.scaled[at] = __bfloat16_as_ushort(__float2bfloat16_rn(in_rank ? __fmul_rn(s, v) : 0.f));
     }
     __syncwarp();
     ad_cluster_sync();  // no CTA ends while another reads its sums
@@ -539,7 +540,8 @@ static cudaError_t launch_ad_down(const DownArgs &a, cudaStream_t st) {
     static_assert(smem >= 64 * (NT * 8 + 4) * 4, "the partial tile fits into the ring");
     // every group's last tile may be partial: at most n / 64 whole tiles and one more per group present
     const int64_t tiles = a.n / 64 + (a.count + 1 < a.n ? a.count + 1 : a.n);
-    // Eight CTAs per tile while all fit at once, else four (28672 columns, rank 64, 4096 tokens: 99 us against 115).
+    // Eight CTAs per tile while all fit at once, for the shortest chain (4096 columns, 100 tokens of 8 adapters: 27.3 us
+    // for the whole call, 29.4 us with four), else four (28672 columns, rank 64, 4096 tokens: 99 us against 115).
     const int64_t slots = 148 * ((int64_t)(228 * 1024) / (int64_t)(smem + 1024));
     const unsigned cl = tiles * kAdCluster <= slots ? kAdCluster : kAdCluster / 2;
     return launch_cluster(adapter_down_kernel<NT, WKM>, dim3((unsigned)tiles, cl), dim3(1, cl), smem, st, a);
@@ -563,7 +565,8 @@ cudaError_t launch_adapter_down_small(const uint16_t *in, int64_t n, int64_t K, 
                                       const int32_t *ids, float *full, uint16_t *scaled, int *status, cudaStream_t st) {
     const SmallArgs a{in, pool->A, (int)n, pool->r, pool->count, K, ids, pool->rank, pool->scale, full, scaled, status};
     const unsigned groups = (unsigned)(n < pool->count ? n : pool->count), jt = (unsigned)((pool->r + 15) / 16);
-    // Clusters of 8 for the shortest chain; of 4 where those would put two CTAs on an SM.
+    // Clusters of 8 for the shortest chain; of 4 where those would put two CTAs on an SM (whole calls of 4096 x 4096, 8 / 4:
+    // one token 12.6 / 13.2 us; 32 tokens of 32 adapters, rank 16: 25.9 / 22.7 us, rank 64: 41 / 38 us).
 #define QLN_AD_SMALL(NT) \
     (groups * jt * 8 <= 148 ? launch_cluster(adapter_down_small_kernel<NT, 8>, dim3(groups, jt, 8), dim3(1, 1, 8), 0, st, a) \
                             : launch_cluster(adapter_down_small_kernel<NT, 4>, dim3(groups, jt, 4), dim3(1, 1, 4), 0, st, a))

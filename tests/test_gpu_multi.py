@@ -224,6 +224,22 @@ def test_infinite_factor_gives_its_own_tokens_the_signed_infinity():
     assert torch.isfinite(Y[c.ids != 1]).all()
 
 
+@pytest.mark.parametrize("n", [5, 32, 40, 300])
+@pytest.mark.parametrize("shape", [(192, 320), (256, 512)])
+def test_rank_zero_adds_nothing_whatever_its_scale(n, shape):
+    c = Case(*shape, n, 3, 16, "random", seed=9)
+    c.ids[0] = 1
+    c.s[1], c.rank = float("inf"), torch.tensor([7, 0, 16], dtype=torch.int32, device="cuda")
+    c.pool = api.AdapterPool(c.A, c.B, c.s, c.rank)
+    at = c.ids == 1
+    Y, U = c.fwd()
+    dX, dA, dB = c.bwd(U=U)
+    c.ids = torch.where(at, -1, c.ids).int()  # the same without an adapter
+    Y0, U0 = c.fwd()
+    assert torch.equal(Y, Y0) and torch.equal(U, U0) and (U[at] == 0).all()
+    assert torch.equal(dX, c.bwd(U=U0)[0]) and (dA[1] == 0).all() and (dB[1] == 0).all()
+
+
 def test_gradients_agree_with_differences():
     """L = sum dY Y is linear in A, in B and in X each, so central differences of the float64 forward are its
     derivatives up to rounding; the kernels' gradients have to give the same along random directions."""
