@@ -7,7 +7,10 @@ or a call fails, an exception is raised.
 
 Function names follow the C entry points: ``nf4_quantize``,
 ``nf4_double_quant``, ``nf4_dequant``, ``qlora_linear_fwd``,
-``qlora_linear_bwd``, plus ``workspace_bytes``, ``codebook``, ``version``.
+``qlora_linear_bwd``; ``qlora_multi_fwd``, ``qlora_multi_bwd`` over an
+``AdapterPool``; ``adamw_step``, and over lists of tensors ``adamw_multi_step``
+(``AdamWTensors``) and ``adamw8_multi_step`` (``AdamW8Tensors``); plus
+``workspace_bytes``, ``codebook``, ``version``.
 """
 import ctypes
 import functools
@@ -431,7 +434,8 @@ class AdapterPool:
 
     A bf16 [count][r][din], B bf16 [count][dout][r], scale fp32 [count], and
     rank int32 [count] or None (every adapter has rank r).  The tensors are
-    checked once and kept; their contents may change between calls."""
+    checked once and their memory is kept: its contents may change between
+    calls (a parameter that is given other memory needs a new pool)."""
 
     def __init__(self, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor, rank: Optional[torch.Tensor] = None):
         if A.dim() != 3 or B.dim() != 3:
@@ -451,11 +455,14 @@ class AdapterPool:
                 raise ValueError(f"{name} is on {t.device}, A on {A.device}")
             if name in ("scale", "rank") and t.numel() != count:
                 raise ValueError(f"{name} holds {t.numel()} elements, needs {count}")
-        self.A, self.B, self.scale, self.rank = A, B, scale, rank
+        # aliases: they hold the memory even if a parameter is given another
+        self._tensors = A.detach(), B.detach(), scale.detach(), None if rank is None else rank.detach()
         self.count, self.r, self.din, self.dout, self.device = count, r, A.shape[2], B.shape[1], A.device
         self.index = A.get_device()  # -1: not a CUDA tensor; the calls refuse it
         self.c = CAdapterPool(A.data_ptr(), B.data_ptr(), scale.data_ptr(), None if rank is None else rank.data_ptr(),
                               count, r)
+
+    A, B, scale, rank = (property(lambda self, i=i: self._tensors[i]) for i in range(4))
 
 
 def _check_multi(w: NF4Weight, pool: AdapterPool, X, ids, others):
@@ -558,8 +565,9 @@ def adamw_step(param: torch.Tensor, grad: torch.Tensor, m: torch.Tensor, v: torc
 class _TensorList:
     """The tensors of a list update, checked once, and their C descriptors.
 
-    Keeps the tensors alive; the update works on their memory as it is then, so
-    gradients are written into the same tensors before each step."""
+    Keeps the tensors' memory; the update works on its contents as they are
+    then, so gradients are written into the same tensors before each step (a
+    tensor that is given other memory, p.data = ..., needs a new list)."""
     _ctype = None
 
     def __init__(self, count, fields):
@@ -579,7 +587,7 @@ class _TensorList:
             ts = [None] * count if ts is None else list(ts)
             if len(ts) != count:
                 raise ValueError(f"{len(ts)} {name} tensors for {count} parameters")
-            self.tensors[name] = ts
+            self.tensors[name] = [None if t is None else t.detach() for t in ts]
             column = []
             for i, (t, n) in enumerate(zip(ts, sizes)):
                 if t is None and name == "param_bf16":

@@ -395,6 +395,7 @@ typedef struct {
  *   ws: at least qln_workspace_bytes(QLN_OP_MULTI_FWD, dout, din, n, r) bytes,
  *   256-byte aligned; byte 0 holds the device status word afterwards.  Calls
  *   that may run at the same time need workspaces of their own.
+ * No output may overlap an input, the workspace or another output.
  * Errors: QLN_ERR_NULL; QLN_ERR_SHAPE (n < 1 or above 2^24; count; r; rows or
  * cols not a multiple of 64); QLN_ERR_ALIGN (16-byte: codes, X, A, B, Y, U_out;
  * 4-byte: ids, scale, rank; ws 256-byte); QLN_ERR_WORKSPACE; QLN_ERR_ARCH.
@@ -413,7 +414,8 @@ QLN_API qln_status qlora_multi_fwd(const qln_nf4_weight *w, const qln_adapter_po
  * Every element of dA and dB is written: zero for adapters without tokens and
  * past an adapter's rank.  Sums run in an order fixed by the sizes and ids.
  * U (nullable) is U_out of the matching forward; when NULL it is recomputed.
- * G and U enter dA and dB with 16 bits of mantissa and fp32 accumulation.
+ * G and U enter dA and dB as the fp32 values they are (three bf16 parts, whose
+ * products with X and dY are exact), with fp32 accumulation.
  * ws: at least qln_workspace_bytes(QLN_OP_MULTI_BWD, dout, din, n, r) bytes.
  * Errors: as qlora_multi_fwd, for dY, dX, dA and dB too.
  */

@@ -105,3 +105,11 @@ def test_calls_refuse_other_lists_steps_and_devices():
         api.adamw_multi_step(t, torch.ones(1), 1e-3)
     with pytest.raises(ValueError, match="CUDA"):
         api.adamw_multi_step(t, torch.ones(1, dtype=torch.int64), 1e-3)
+
+
+def test_lists_keep_the_memory_they_were_made_of():
+    d = _t()
+    t = api.AdamWTensors(**d)
+    at = d["params"][1].data_ptr()
+    d["params"][1].data = torch.ones_like(d["params"][1])
+    assert t.array[1].param == at == t.tensors["param"][1].data_ptr() != d["params"][1].data_ptr()

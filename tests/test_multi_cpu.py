@@ -96,6 +96,15 @@ def test_pool_is_checked():
             _pool(**bad)
 
 
+def test_pool_keeps_the_memory_it_was_made_of():
+    A = torch.nn.Parameter(torch.zeros(3, 16, 256, dtype=torch.bfloat16))
+    pool = _pool(A=A)
+    A.data = torch.ones(3, 16, 256, dtype=torch.bfloat16)
+    assert pool.c.A == pool.A.data_ptr() != A.data_ptr() and (pool.A == 0).all()
+    with pytest.raises(AttributeError):
+        pool.A = A
+
+
 def test_calls_check_shapes_types_and_device():
     pool = _pool()
     w = api.NF4Weight(codes=torch.zeros(128 * 128, dtype=torch.uint8), rows=128, cols=256, absmax=torch.zeros(512))
