@@ -20,25 +20,28 @@ namespace qln {
 //                     and at the end those without an adapter (group `count`)
 //   start [count + 2] first place of each group in order
 //   tiles [count + 2] first 64-token tile of each group (tiles never mix)
-// Warp w owns the w-th of 32 contiguous token ranges and a histogram of its
+// Warp w owns the w-th of nw contiguous token ranges and a histogram of its
 // own, so places follow from two passes over the ids and one scan, and do not
-// depend on timing.  Latency-bound: a few dependent reads of the ids.
+// depend on timing.  Latency-bound: a few dependent reads of the ids, and loops
+// over the histograms, so there are no more of them than ranges of 32 tokens.
 // ===========================================================================
 constexpr int kPlanWarps = 32;
 
-__global__ void __launch_bounds__(kPlanWarps * 32) adapter_plan_kernel(const int32_t *__restrict__ ids, int n, int count,
+static int plan_ranges(int64_t n) { return n >= 32 * kPlanWarps ? kPlanWarps : (int)((n + 31) / 32); }
+
+__global__ void __launch_bounds__(kPlanWarps * 32) adapter_plan_kernel(const int32_t *__restrict__ ids, int n, int count, int nw,
                                                                        int32_t *__restrict__ order,
                                                                        int32_t *__restrict__ start,
                                                                        int32_t *__restrict__ tiles, int *status) {
-    extern __shared__ int hist[];  // [warp][count]
+    extern __shared__ int hist[];  // [nw][count]
     __shared__ int wsum[2][kPlanWarps], s_none[kPlanWarps];
     pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) *status = QLN_OK;  // the first kernel of the call clears the status word
-    for (int i = tid; i < kPlanWarps * count; i += kPlanWarps * 32) hist[i] = 0;
+    for (int i = tid; i < nw * count; i += kPlanWarps * 32) hist[i] = 0;
     __syncthreads();
-    const int t0 = (int)((int64_t)n * warp / kPlanWarps), t1 = (int)((int64_t)n * (warp + 1) / kPlanWarps);
+    const int t0 = warp < nw ? (int)((int64_t)n * warp / nw) : n, t1 = warp < nw ? (int)((int64_t)n * (warp + 1) / nw) : n;
     int none = 0;  // tokens of this warp's range without an adapter
     for (int tb = t0; tb < t1; tb += 32) {
         const int t = tb + lane;
@@ -52,10 +55,15 @@ __global__ void __launch_bounds__(kPlanWarps * 32) adapter_plan_kernel(const int
     // thread a: this adapter's places within the warps' ranges, and its total
     int total = 0;
     if (tid < count)
-        for (int w = 0; w < kPlanWarps; ++w) {
-            const int c = hist[w * count + tid];
-            hist[w * count + tid] = total;
-            total += c;
+        for (int w0 = 0; w0 < nw; w0 += 8) {
+            int c[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) c[u] = w0 + u < nw ? hist[(w0 + u) * count + tid] : 0;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (w0 + u < nw) hist[(w0 + u) * count + tid] = total;
+                total += c[u];
+            }
         }
     // block-wide exclusive scans of the totals and of their 64-token tiles
     int v[2] = {total, (total + 63) >> 6}, inc[2];
@@ -71,16 +79,11 @@ __global__ void __launch_bounds__(kPlanWarps * 32) adapter_plan_kernel(const int
     }
     __syncthreads();
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        int base = 0;
-        for (int w = 0; w < warp; ++w) base += wsum[q][w];
-        inc[q] += base - v[q];  // exclusive
-    }
-    int nall = 0, nbase = 0;  // tokens without an adapter: all, and of the warps before this one
-    for (int w = 0; w < kPlanWarps; ++w) {
-        nbase += w < warp ? s_none[w] : 0;
-        nall += s_none[w];
-    }
+    for (int q = 0; q < 2; ++q)  // exclusive
+        inc[q] += __reduce_add_sync(0xffffffffu, lane < warp ? wsum[q][lane] : 0) - v[q];
+    // tokens without an adapter: all, and of the warps before this one
+    const int nall = __reduce_add_sync(0xffffffffu, s_none[lane]);
+    const int nbase = __reduce_add_sync(0xffffffffu, lane < warp ? s_none[lane] : 0);
     if (tid < count) {
         start[tid] = inc[0];
         tiles[tid] = inc[1];
@@ -90,7 +93,14 @@ __global__ void __launch_bounds__(kPlanWarps * 32) adapter_plan_kernel(const int
             tiles[count] = inc[1] + v[1];
             tiles[count + 1] = inc[1] + v[1] + ((nall + 63) >> 6);
         }
-        for (int w = 0; w < kPlanWarps; ++w) hist[w * count + tid] += inc[0];
+        for (int w0 = 0; w0 < nw; w0 += 8) {
+            int c[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) c[u] = w0 + u < nw ? hist[(w0 + u) * count + tid] : 0;
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (w0 + u < nw) hist[(w0 + u) * count + tid] = c[u] + inc[0];
+        }
     }
     __syncthreads();
     int at_none = n - nall + nbase;
@@ -109,15 +119,36 @@ __global__ void __launch_bounds__(kPlanWarps * 32) adapter_plan_kernel(const int
     }
 }
 
-// The group whose tiles hold tile i: tiles[a] <= i < tiles[a + 1].
-__device__ __forceinline__ int tile_adapter(const int32_t *tiles, int count, int i) {
-    int lo = 0, hi = count + 1;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(tiles + mid) <= i) lo = mid;
-        else hi = mid;
+// Tile i of the plan: its group, its first place in order, its tokens (0: there
+// is no such tile).  For a whole warp, which reads 32 entries of the tables at a
+// time: one dependent read for up to 30 adapters, three at most (a bisection
+// takes up to ten).
+struct PlanTile {
+    int a, p0, rows;
+};
+__device__ __forceinline__ PlanTile plan_tile(const int32_t *start, const int32_t *tiles, int count, int i) {
+    const int lane = threadIdx.x & 31;
+    int a, s0, s1, v0, all;
+    if (count + 2 <= 32) {
+        const int k = min(lane, count + 1), v = __ldg(tiles + k), s = __ldg(start + k);
+        a = 31 - __clz(__ballot_sync(0xffffffffu, lane <= count && v <= i));  // the last with tiles[a] <= i
+        all = __shfl_sync(0xffffffffu, v, count + 1);
+        v0 = __shfl_sync(0xffffffffu, v, a);
+        s0 = __shfl_sync(0xffffffffu, s, a);
+        s1 = __shfl_sync(0xffffffffu, s, a + 1);
+    } else {
+        static_assert(QLN_MAX_ADAPTERS <= 32 * 33 - 1, "two levels");
+        all = __ldg(tiles + count + 1);
+        const int b = 33 * (31 - __clz(__ballot_sync(0xffffffffu, 33 * lane <= count && __ldg(tiles + min(33 * lane, count)) <= i)));
+        const int k = b + 1 + lane;
+        a = b + __popc(__ballot_sync(0xffffffffu, k <= count && __ldg(tiles + min(k, count)) <= i));
+        v0 = __ldg(tiles + a);
+        s0 = __ldg(start + a);
+        s1 = __ldg(start + a + 1);
     }
-    return lo;
+    if (i >= all) return PlanTile{0, 0, 0};
+    const int p0 = s0 + 64 * (i - v0);
+    return PlanTile{a, p0, min(64, s1 - p0)};
 }
 
 __device__ __forceinline__ int adapter_rank(const int32_t *rank, int a, int r) {
@@ -192,12 +223,11 @@ __global__ void __launch_bounds__(128) adapter_down_kernel(const DownArgs p) {
     constexpr int STAGE = 64 * kAdLd + (WKM ? 64 * WKLD : WR * kAdLd);
     pdl_wait();
     pdl_trigger();
-    const int tile = blockIdx.x, count = p.count, r = p.r;
+    const int count = p.count, r = p.r;
     const int64_t n = p.n, K = p.K;
-    if (tile >= __ldg(p.tiles + count + 1)) return;  // the whole cluster
-    const int a = tile_adapter(p.tiles, count, tile);
-    const int p0 = __ldg(p.start + a) + 64 * (tile - __ldg(p.tiles + a));
-    const int rows = min(64, __ldg(p.start + a + 1) - p0);
+    const PlanTile pt = plan_tile(p.start, p.tiles, count, blockIdx.x);
+    const int a = pt.a, p0 = pt.p0, rows = pt.rows;
+    if (rows == 0) return;  // the whole cluster
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, part = blockIdx.y;
     const int cl = gridDim.y, own = 64 / cl;  // CTAs of the cluster, rows that each finishes
     if (a == count) {  // tokens without an adapter
@@ -207,6 +237,8 @@ __global__ void __launch_bounds__(128) adapter_down_kernel(const DownArgs p) {
         return;
     }
     const uint16_t *wt = p.pool + (int64_t)a * r * K;
+    const int rk = adapter_rank(p.rank, a, r);
+    const float s = __ldg(p.scale + a);
     const int g = lane >> 2, c = lane & 3;
     const int nch = (int)(K / 64);
     const int ch0 = nch * part / cl, ch1 = nch * (part + 1) / cl;
@@ -310,8 +342,6 @@ __global__ void __launch_bounds__(128) adapter_down_kernel(const DownArgs p) {
             *reinterpret_cast<float2 *>(part_s + (16 * warp + g + 8 * h) * PLD + 8 * nt + 2 * c) =
                 make_float2(sum[nt][2 * h], sum[nt][2 * h + 1]);
     ad_cluster_sync();
-    const int rk = adapter_rank(p.rank, a, r);
-    const float s = __ldg(p.scale + a);
     const uint32_t base = smem_u32(part_s);
     const int64_t plane = n * r;
     for (int i = tid; i < own * r; i += 128) {
@@ -499,12 +529,13 @@ AdapterPlan adapter_plan_at(void *base, int64_t n) {
 }
 
 cudaError_t launch_adapter_plan(const int32_t *ids, int64_t n, int count, const AdapterPlan &p, int *status, cudaStream_t st) {
-    const size_t smem = (size_t)kPlanWarps * count * sizeof(int);
+    const int nw = plan_ranges(n);
+    const size_t smem = (size_t)nw * count * sizeof(int);
     if (smem > 48 * 1024) {
         cudaError_t e = cudaFuncSetAttribute(adapter_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    return launch_pdl(adapter_plan_kernel, dim3(1), dim3(kPlanWarps * 32), smem, st, ids, (int)n, count, p.order, p.start,
+    return launch_pdl(adapter_plan_kernel, dim3(1), dim3(kPlanWarps * 32), smem, st, ids, (int)n, count, nw, p.order, p.start,
                       p.tiles, status);
 }
 

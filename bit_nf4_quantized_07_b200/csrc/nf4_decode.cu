@@ -701,7 +701,7 @@ static bool df_plan_s(int64_t T, int64_t KB, int r, int NT, int S, int64_t Q, bo
     const int64_t nkb_min = KB / S;
     // A items (U): at most 32, ideally enough sub-ranges of one block or more for every warp to
     // take one; fewer when their partials do not fit
-    int nsubA0 = (int)(nkb_min < kDfWarps ? nkb_min : kDfWarps);
+    int nsubA0 = multi ? 1 : (int)(nkb_min < kDfWarps ? nkb_min : kDfWarps);
     while (nsubA0 > 1 && L.JT * nsubA0 > 2 * kDfWarps) nsubA0 /= 2;
     // sub-ranges: fewest code boxes per warp (items of the first epoch spread
     // over 16 warps; a box carries 4 blocks whether or not all are used), ties
