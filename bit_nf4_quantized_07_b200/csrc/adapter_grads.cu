@@ -8,11 +8,11 @@
 //
 // HBM-bound (P is read once, Q is narrow), so everything else has to stay out
 // of the way of the loads.  An item is 128 MT rows m of one adapter over all of
-// its tokens, K in steps of 64 gathered tokens; a CTA works through its share of
-// the items without draining its ring in between.  Producer warps copy
+// its tokens, K in steps of 64 gathered tokens; a CTA works through every
+// gridDim.x-th item without draining its ring in between.  Producer warps copy
 // the token rows by cp.async into swizzled tiles (a row of P or Q is one K of an
 // MN-major operand, so nothing is transposed), their token numbers read two
-// steps ahead; one thread issues the MMAs; 4 MT warps add up and store.  Q
+// steps ahead; one thread issues the MMAs; four warps or eight add up and store.  Q
 // enters as three bf16 parts (what an fp32 value holds), three MMAs each; the
 // first part has an accumulator of its own, because the tensor cores' running
 // sums truncate at every addition.  For the same reason the accumulators, two
@@ -40,7 +40,8 @@ struct GrCfg {
     static constexpr uint32_t kPBytes = MT * 16384u;
     static constexpr uint32_t kQPart = kQBlocks * kGrBK * kRowB;
     static constexpr uint32_t kStage = kPBytes + 3 * kQPart;
-    static constexpr int kSumWarps = 4 * MT;        // a TMEM lane quadrant of a sub-tile each
+    static constexpr int kCols = NB > 64 ? 64 : NB;  // columns that a sum warp keeps in registers
+    static constexpr int kSumWarps = 4 * MT * (NB / kCols);  // a TMEM lane quadrant of a sub-tile (or half of its columns) each
     static constexpr int kProdWarps = 8;            // then the producers, then the issuer
     static constexpr int kThreads = (kSumWarps + kProdWarps + 1) * 32;
     static constexpr int kCtas = NB <= 32 ? 2 : 1;  // per SM
@@ -93,28 +94,23 @@ __global__ void __launch_bounds__(GrCfg<NB, MT>::kThreads, GrCfg<NB, MT>::kCtas)
         }
         s_order[ahead] = lane;
     }
-    struct Item {  // 128 MT rows of one adapter
-        int a, p0, cnt;
-        bool dA;
-        int64_t M, m0;
+    struct Item {  // 128 MT rows of one adapter: tile counts dB's, then dA's
+        int a, p0, cnt, tile;
+        __device__ bool dA(const GradArgs &p) const { return tile >= p.tilesB; }
+        __device__ int64_t M(const GradArgs &p) const { return dA(p) ? p.M[1] : p.M[0]; }
+        __device__ int64_t m0(const GradArgs &p) const { return (int64_t)(dA(p) ? tile - p.tilesB : tile) * (128 * MT); }
     };
     auto item_at = [&](int i) {
-        Item t{0, 0, 0, false, 0, 0};
+        Item t{0, 0, 0, 0};
         if (i < items) {
             t.a = i / p.tiles;
-            const int tile = i - t.a * p.tiles;
+            t.tile = i - t.a * p.tiles;
             if (p.count <= 32) t.a = s_order[t.a];
-            t.dA = tile >= p.tilesB;
-            t.M = t.dA ? p.M[1] : p.M[0];
-            t.m0 = (int64_t)(t.dA ? tile - p.tilesB : tile) * 128 * MT;
             t.p0 = __ldg(p.start + t.a);
             t.cnt = __ldg(p.start + t.a + 1) - t.p0;
         }
         return t;
     };
-    const int G = (int)gridDim.x, cta = (int)blockIdx.x;
-    // This CTA's k-th item (past the last: none).  Every other round runs backwards, so that a CTA gets long and short ones.
-    auto nth = [&](int k) { return k * G + (k & 1 ? G - 1 - cta : cta); };
     auto steps_of = [](const Item &t) { return (t.cnt + kGrBK - 1) / kGrBK; };
 
     if (tid == 0) {
@@ -148,31 +144,22 @@ __global__ void __launch_bounds__(GrCfg<NB, MT>::kThreads, GrCfg<NB, MT>::kCtas)
         // once its copies have landed, two steps after their issue.
         constexpr int kLag = S - 2;
         const int pt = tid - 32 * kProd, c = pt & 15, r0 = pt >> 4;
-        struct Step {  // one step's rows: tokens (-1: none), where they are read
-            int tok[4];
-            const uint16_t *P, *Q;
-            int64_t M;
-            bool in0, in1;  // the chunk's columns of the two sub-tiles exist
-            bool live;
+        struct Step {  // one step: its tokens (-1: none) and its item's tile (-1: no step)
+            int tok[4], tile;
         };
-        int rnd = 0, st = 0, left = 0;  // the look-ahead: its item's next step, steps left
-        Item it = item_at(nth(0)), nx = item_at(nth(1));
+        int next_item = blockIdx.x, st = 0, left = 0;  // the look-ahead: its item's next step, steps left
+        Item it = item_at(next_item), nx = item_at(next_item + gridDim.x);
         left = steps_of(it);
         auto look = [&](Step &x) {
-            while (left == 0 && rnd * G < items) {
-                ++rnd;
+            while (left == 0 && next_item < items) {
+                next_item += gridDim.x;
                 it = nx;
-                nx = item_at(nth(rnd + 1));
+                nx = item_at(next_item + gridDim.x);
                 left = steps_of(it);
                 st = 0;
             }
-            x.live = left > 0;
-            if (!x.live) return;
-            x.M = it.M;
-            x.P = (it.dA ? p.P[1] : p.P[0]) + it.m0 + 8 * c;
-            x.Q = it.dA ? p.Q[1] : p.Q[0];
-            x.in0 = it.m0 + 8 * c < it.M;
-            x.in1 = it.m0 + 128 + 8 * c < it.M;
+            x.tile = left > 0 ? it.tile : -1;
+            if (left == 0) return;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int q = st * kGrBK + r0 + 16 * i;
@@ -190,7 +177,7 @@ __global__ void __launch_bounds__(GrCfg<NB, MT>::kThreads, GrCfg<NB, MT>::kCtas)
         look(n1);
         int k = 0, done = 0;  // steps issued, handed over
         bool ok = true;
-        while (cur.live) {
+        while (cur.tile >= 0) {
             const int s = k % S;
             ok = tc::mbar_wait_bounded(empty(s), ((uint32_t)(k / S) & 1u) ^ 1u, abort_flag, kGrWaitNs);
             if (!ok) {
@@ -198,14 +185,18 @@ __global__ void __launch_bounds__(GrCfg<NB, MT>::kThreads, GrCfg<NB, MT>::kCtas)
                 break;
             }
             const uint32_t sP = sbase + s * C::kStage, sQ = sP + C::kPBytes;
+            const Item of{0, 0, 0, cur.tile};
+            const bool dA = of.dA(p);
+            const int64_t M = of.M(p), m = of.m0(p) + 8 * c;  // this thread's columns of P: m, and 128 further
+            const uint16_t *const P = (dA ? p.P[1] : p.P[0]) + m, *const Q = dA ? p.Q[1] : p.Q[0];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int row = r0 + 16 * i, t = cur.tok[i], r7 = r0 & 7;  // row % 8
                 const bool in = t >= 0;
-                const uint16_t *src = cur.P + (int64_t)t * cur.M;
+                const uint16_t *src = P + (int64_t)t * M;
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    const bool ok16 = in && (mt ? cur.in1 : cur.in0);
+                    const bool ok16 = in && m + 128 * mt < M;
                     // 64-wide blocks of m, 8192 bytes each
                     const uint32_t dst = sP + mt * 16384 + (c >> 3) * 8192 + row * 128 + (((c & 7) ^ r7) << 4);
                     cp_async16_to(dst, ok16 ? src + 128 * mt : p.P[0], ok16 ? 16 : 0);
@@ -219,7 +210,7 @@ __global__ void __launch_bounds__(GrCfg<NB, MT>::kThreads, GrCfg<NB, MT>::kCtas)
                     const int swz = C::kRowB == 128 ? r7 : C::kRowB == 64 ? (row >> 1) & 3 : (row >> 2) & 1;
                     const uint32_t dst = sQ + part * C::kQPart + (ck >> 3) * (kGrBK * 128) + row * C::kRowB +
                                          (((ck & 7) ^ swz) << 4);
-                    cp_async16_to(dst, ok16 ? cur.Q + part * p.plane + (int64_t)t * r + 8 * ck : p.P[0], ok16 ? 16 : 0);
+                    cp_async16_to(dst, ok16 ? Q + part * p.plane + (int64_t)t * r + 8 * ck : p.P[0], ok16 ? 16 : 0);
                 }
             }
             cp_async_commit();
@@ -238,10 +229,10 @@ __global__ void __launch_bounds__(GrCfg<NB, MT>::kThreads, GrCfg<NB, MT>::kCtas)
             const uint32_t idesc = tc::idesc_bf16_f32(128, NB, true, true);
             int k = 0, grp = 0;  // steps and groups so far
             bool ok = true;
-            Item nx = item_at(nth(0));
-            for (int rnd = 0; ok && rnd * G < items; ++rnd) {
+            Item nx = item_at(blockIdx.x);
+            for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
                 const int steps = steps_of(nx);
-                nx = item_at(nth(rnd + 1));
+                nx = item_at(i + gridDim.x);
                 for (int st = 0; st < steps; ++st, ++k) {
                     const int s = k % S, b = grp & 1;
                     const bool first = st % kGrGroup == 0, last = st % kGrGroup == kGrGroup - 1 || st == steps - 1;
@@ -274,16 +265,19 @@ __global__ void __launch_bounds__(GrCfg<NB, MT>::kThreads, GrCfg<NB, MT>::kCtas)
         }
     } else {
         // ------------------------------------------------------------ sums and results
-        const int mt = warp >> 2, quad = warp & 3;
+        constexpr int NC = C::kCols;
+        const int mt = (warp >> 2) % MT, quad = warp & 3, col0 = (warp >> 2) / MT * NC;
         int grp = 0;
         bool ok = true;
-        Item nx = item_at(nth(0));
-        for (int rnd = 0; ok && rnd * G < items; ++rnd) {
+        Item nx = item_at(blockIdx.x);
+        for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
             const Item t = nx;
-            nx = item_at(nth(rnd + 1));
-            float sum[NB];
+            nx = item_at(i + gridDim.x);
+            const int rk0 = p.rank ? __ldg(p.rank + t.a) : r;
+            const float s = __ldg(p.scale + t.a);
+            float sum[NC];
 #pragma unroll
-            for (int j = 0; j < NB; ++j) sum[j] = 0.f;
+            for (int j = 0; j < NC; ++j) sum[j] = 0.f;
             for (int g = (steps_of(t) + kGrGroup - 1) / kGrGroup; g > 0; --g, ++grp) {
                 const int b = grp & 1;
                 ok = tc::mbar_wait_bounded(acc_full(b), (uint32_t)(grp / 2) & 1u, abort_flag, kGrWaitNs);
@@ -291,9 +285,9 @@ __global__ void __launch_bounds__(GrCfg<NB, MT>::kThreads, GrCfg<NB, MT>::kCtas)
                 ok = __all_sync(0xffffffffu, ok);  // tcgen05.ld is warp-collective
                 if (!ok) break;
                 tc::tc_fence_after();
-                const uint32_t base = tmem_d + ((uint32_t)(quad * 32) << 16) + (uint32_t)((b * MT + mt) * 2 * NB);
+                const uint32_t base = tmem_d + ((uint32_t)(quad * 32) << 16) + (uint32_t)((b * MT + mt) * 2 * NB + col0);
 #pragma unroll
-                for (int j0 = 0; j0 < NB; j0 += 8) {
+                for (int j0 = 0; j0 < NC; j0 += 8) {
                     uint32_t v[8], w[8];
                     tc::tmem_ld_32x32b_x8(base + j0, v);
                     tc::tmem_ld_32x32b_x8(base + NB + j0, w);
@@ -306,24 +300,23 @@ __global__ void __launch_bounds__(GrCfg<NB, MT>::kThreads, GrCfg<NB, MT>::kCtas)
                 tc::mbar_arrive(acc_empty(b));
             }
             if (!ok) break;
-            const int rk0 = p.rank ? __ldg(p.rank + t.a) : r, rk = t.cnt > 0 ? min(max(rk0, 0), r) : 0;
-            const float s = __ldg(p.scale + t.a);
-            const int64_t m = t.m0 + 128 * mt + quad * 32 + lane;
-            float *out = (t.dA ? p.C[1] : p.C[0]) + (int64_t)t.a * t.M * r;
-            if (m < t.M && t.dA) {  // dA [r][din]: consecutive m per j
+            const int rk = t.cnt > 0 ? min(max(rk0, 0), r) : 0;
+            const int64_t M = t.M(p), m = t.m0(p) + 128 * mt + quad * 32 + lane;
+            float *out = (t.dA(p) ? p.C[1] : p.C[0]) + (int64_t)t.a * M * r;
+            if (m < M && t.dA(p)) {  // dA [r][din]: consecutive m per j
 #pragma unroll
-                for (int j = 0; j < NB; ++j)
-                    if (j < r) out[(int64_t)j * t.M + m] = j < rk ? __fmul_rn(s, sum[j]) : 0.f;
-            } else if (m < t.M) {   // dB [dout][r]: a row of r per m (r is a multiple of 8)
+                for (int j = 0; j < NC; ++j)
+                    if (col0 + j < r) out[(int64_t)(col0 + j) * M + m] = col0 + j < rk ? __fmul_rn(s, sum[j]) : 0.f;
+            } else if (m < M) {   // dB [dout][r]: a row of r per m (r is a multiple of 8)
 #pragma unroll
-                for (int j = 0; j < NB; j += 4)
-                    if (j < r) {
+                for (int j = 0; j < NC; j += 4)
+                    if (col0 + j < r) {
                         float4 v;
-                        v.x = j < rk ? __fmul_rn(s, sum[j]) : 0.f;
-                        v.y = j + 1 < rk ? __fmul_rn(s, sum[j + 1]) : 0.f;
-                        v.z = j + 2 < rk ? __fmul_rn(s, sum[j + 2]) : 0.f;
-                        v.w = j + 3 < rk ? __fmul_rn(s, sum[j + 3]) : 0.f;
-                        *reinterpret_cast<float4 *>(out + m * r + j) = v;
+                        v.x = col0 + j < rk ? __fmul_rn(s, sum[j]) : 0.f;
+                        v.y = col0 + j + 1 < rk ? __fmul_rn(s, sum[j + 1]) : 0.f;
+                        v.z = col0 + j + 2 < rk ? __fmul_rn(s, sum[j + 2]) : 0.f;
+                        v.w = col0 + j + 3 < rk ? __fmul_rn(s, sum[j + 3]) : 0.f;
+                        *reinterpret_cast<float4 *>(out + m * r + col0 + j) = v;
                     }
             }
         }
