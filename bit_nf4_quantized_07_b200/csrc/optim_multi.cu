@@ -10,18 +10,22 @@
 //   p = p - (lr / (1 - b1^t)) m / (sqrt(v / (1 - b2^t)) + eps)
 //
 // 8-bit states.  Blocks of 256 consecutive elements of a tensor share one fp32
-// scale b = max|x| / 448 and hold E4M3 codes of x (448 / max|x|), the group format that
-// the double quantization uses for the block constants.  The first moment is
-// held as x = m, the second as x = sqrt(v): its square spans 2^36 within a
-// block instead of 2^18.  A nonzero sqrt(v) is never rounded to zero (it takes
-// the smallest code): a zero denominator under a nonzero m would turn the step
-// into lr m / eps.  The update itself runs in fp32 on the restored states, and
-// uses the new v before it is rounded.  Per element its 18 bytes leave about
-// 100 issue slots at the HBM rate: with correctly rounded quotients, roots and
-// separate products the step needed all of them (448 tensors, 40 M elements:
-// 226 us, 49 % of the HBM rate); it uses fused products, one division per block
-// for the codes, and the hardware's approximate root and quotient (2 and 4
-// units of 2^-24, next to a code's 2^-4).
+// scale b = max|x| / 448 (formed as max|x| times fp32(1/448)) and hold the E4M3
+// codes of fp32(x / b), the group format that the double quantization uses for
+// the block constants.  The first moment is held as x = m, the second as
+// x = sqrt(v): its square spans 2^36 within a block instead of 2^18.  A nonzero
+// sqrt(v) is never rounded to zero (it takes the smallest code): a zero
+// denominator under a nonzero m would turn the step into lr m / eps.  The update
+// itself runs in fp32 on the restored states, and uses the new v before it is
+// rounded.  Per element its 18 bytes leave about 100 issue slots at the HBM rate:
+// with correctly rounded quotients and roots throughout, the step needed all of
+// them (448 tensors, 40 M elements: 226 us, 49 % of the HBM rate).  So the step
+// takes the hardware's approximate root and quotient (2 and 4 units of 2^-24),
+// and the codes come from a product with 1 / b; where a value lies so near to the
+// middle between two codes that those errors could decide (in one warp of a
+// hundred), the warp forms its roots and quotients again, correctly rounded.  A
+// code is a sixteenth of its value: one that fell the other way by an error of
+// 2^-23 would be seen in the steps after it.
 //
 // Both kernels are HBM-bound.  The tensors' pointers travel as a kernel
 // parameter (up to 32 KB), so nothing is copied or allocated and a captured
@@ -183,26 +187,35 @@ __device__ __forceinline__ uint32_t e4m3x4_pack(const float *y) {
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
     return lo | (hi << 16);
 }
-// One element; x: the restored root of v on entry, the new one on return.
-__device__ __forceinline__ void mt_elem8(float &p, float g, float &m, float &x, const MtArgs &a, const MtStep &s,
+// sqrt(x) within 2 units of 2^-24.
+__device__ __forceinline__ float root_approx(float x) {
+    float y;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// One element; v: the restored root of v on entry, the new v on return.
+__device__ __forceinline__ void mt_elem8(float &p, float g, float &m, float &v, const MtArgs &a, const MtStep &s,
                                          float decay) {
-    m = __fmaf_rn(a.b1, m, __fmul_rn(1.0f - a.b1, g));
-    const float v = __fmaf_rn(a.b2, __fmul_rn(x, x), __fmul_rn(__fmul_rn(1.0f - a.b2, g), g));
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(x) : "f"(v));
-    const float denom = __fmaf_rn(x, s.inv_sqrt_bc2, a.eps);
+    m = __fmaf_rn(1.0f - a.b1, g, __fmul_rn(a.b1, m));
+    v = __fmaf_rn(1.0f - a.b2, __fmul_rn(g, g), __fmul_rn(a.b2, __fmul_rn(v, v)));
+    const float denom = __fmaf_rn(root_approx(v), s.inv_sqrt_bc2, a.eps);
     p = __fmaf_rn(-s.step_size, __fdividef(m, denom), __fmul_rn(p, decay));
 }
 constexpr uint32_t kInfBits = 0x7f800000u;
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
-// 448 / max and max / 448 of a block; a block whose quotient overflows (max
-// below about 2^-119) is stored as zeros.
-__device__ __forceinline__ void block_scale(uint32_t max_bits, float &inv, float &b) {
-    const float m = __uint_as_float(max_bits);
-    inv = __fdiv_rn(kE4m3Max, m);
-    const bool ok = __float_as_uint(inv) < kInfBits;
-    inv = ok ? inv : 0.f;
-    b = ok ? __fdiv_rn(m, kE4m3Max) : 0.f;
+// A block's scale b, and 1 / b (0 if b is 0; infinite if b is below about 2^-128).
+__device__ __forceinline__ void block_scale(float top, float &inv, float &b) {
+    b = __fmul_rn(top, 1.0f / kE4m3Max);
+    inv = b > 0.f ? __frcp_rn(b) : 0.f;
+}
+// Whether the code of |y| could depend on an error of 8 units in its last place: then its mantissa lies that near to the
+// middle between two codes, 0x80000 in the 20 bits below a code's three.  Codes below 2^-6 have the spacing of those
+// from 2^-6 to 2^-5.
+__device__ __forceinline__ bool near_middle(float y) {
+    float z = fabsf(y);
+    z = z < 0.015625f ? z + 0.015625f : z;
+    return ((__float_as_uint(z) + 0x80008u) & 0xfffffu) <= 16u;
 }
 
 // A warp takes one block per step and requests the next one's 2.5 KB before it
@@ -286,9 +299,24 @@ adamw8_multi_kernel(const __grid_constant__ MtTable<qln_adamw8_tensor, N> T) {
         uint32_t am = 0, av = 0;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            mt_elem8(p[k], g[k], m[k], v[k], T.a, S, decay);  // v: the root of v
+            mt_elem8(p[k], g[k], m[k], v[k], T.a, S, decay);
             am = max(am, abs_bits(m[k]));
             av = max(av, abs_bits(v[k]));
+        }
+        if (whole) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                *(reinterpret_cast<float4 *>(t.param + e) + h) = make_float4(p[4 * h], p[4 * h + 1], p[4 * h + 2], p[4 * h + 3]);
+            if (t.param_bf16)
+                *reinterpret_cast<uint4 *>(t.param_bf16 + e) =
+                    make_uint4(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]), pack_bf16x2(p[4], p[5]), pack_bf16x2(p[6], p[7]));
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < left) {
+                    t.param[e + k] = p[k];
+                    if (t.param_bf16) t.param_bf16[e + k] = __bfloat16_as_ushort(__float2bfloat16_rn(p[k]));
+                }
         }
         am = __reduce_max_sync(0xffffffffu, am);
         av = __reduce_max_sync(0xffffffffu, av);
@@ -304,14 +332,25 @@ adamw8_multi_kernel(const __grid_constant__ MtTable<qln_adamw8_tensor, N> T) {
             av = __reduce_max_sync(0xffffffffu, av);
         }
         float im, iv, nm, nv;
-        block_scale(am, im, nm);
-        block_scale(av, iv, nv);
+        block_scale(__uint_as_float(am), im, nm);
+        block_scale(__fsqrt_rn(__uint_as_float(av)), iv, nv);  // the largest root: the root is monotone
         float ym[8], yv[8];
+        bool again = __float_as_uint(fmaxf(im, iv)) >= kInfBits;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             ym[k] = __fmul_rn(m[k], im);
-            yv[k] = fmaxf(__fmul_rn(v[k], iv), v[k] > 0.f ? 0.001953125f : 0.f);  // 2^-9, the smallest code
+            yv[k] = __fmul_rn(root_approx(v[k]), iv);
+            again |= near_middle(ym[k]) | near_middle(yv[k]);
         }
+        if (__any_sync(0xffffffffu, again)) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                ym[k] = nm > 0.f ? __fdiv_rn(m[k], nm) : 0.f;
+                yv[k] = nv > 0.f ? __fdiv_rn(__fsqrt_rn(v[k]), nv) : 0.f;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) yv[k] = fmaxf(yv[k], v[k] > 0.f ? 0.001953125f : 0.f);  // 2^-9, the smallest code
         if (odd) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -329,20 +368,12 @@ adamw8_multi_kernel(const __grid_constant__ MtTable<qln_adamw8_tensor, N> T) {
         if (whole) {
             *reinterpret_cast<uint2 *>(t.m + e) = mo;
             *reinterpret_cast<uint2 *>(t.v + e) = vo;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                *(reinterpret_cast<float4 *>(t.param + e) + h) = make_float4(p[4 * h], p[4 * h + 1], p[4 * h + 2], p[4 * h + 3]);
-            if (t.param_bf16)
-                *reinterpret_cast<uint4 *>(t.param_bf16 + e) =
-                    make_uint4(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]), pack_bf16x2(p[4], p[5]), pack_bf16x2(p[6], p[7]));
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 if (k < left) {
-                    t.param[e + k] = p[k];
                     t.m[e + k] = (uint8_t)((k < 4 ? mo.x : mo.y) >> (8 * (k & 3)));
                     t.v[e + k] = (uint8_t)((k < 4 ? vo.x : vo.y) >> (8 * (k & 3)));
-                    if (t.param_bf16) t.param_bf16[e + k] = __bfloat16_as_ushort(__float2bfloat16_rn(p[k]));
                 }
         }
     }

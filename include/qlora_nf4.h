@@ -517,9 +517,8 @@ typedef struct {
  * Defined by the passages that qln_adamw_step cites; the pages do not describe
  * 8-bit states.  They are held in the library's 8-bit group format
  * (QLN_DQ_E4M3, without the mean): the 256 elements of a block (the last block
- * of a tensor may be partial) share b = fp32(max|x| / 448), and an element's
- * code is E4M3(fp32(x * fp32(448 / max|x|))), round to nearest even; a block
- * whose quotient overflows fp32 has b = 0 and codes 0.  The first
+ * of a tensor may be partial) share b = fp32(max|x| * fp32(1/448)), and an
+ * element's code is E4M3(fp32(x / b)), round to nearest even, or 0 if b is.  The first
  * moment is held as x = m, the second as x = sqrt(v).  A sqrt(v) above zero
  * never takes code 0: it is raised to the smallest code (2^-9).
  * A step restores m = fp32(b code) and v = fp32(fp32(b code)^2), updates as

@@ -12,9 +12,9 @@ the fp32 values themselves:
 then the square: 3 u on v) before the step, which adds u |b1 m| to m, 3 u to v
 and 2 u to d.  That kernel takes the approximate root (2 u instead of u) and
 quotient (4 u instead of u), so its step is within 16 u.  A code is the nearest
-E4M3 value to y = x 448 / max: half a step is 2^-4 |y|, below 2^-6 the fixed
-2^-10; the quotient, the product and the scale it is compared with have a
-rounding each (3 u); a root raised to the smallest code is off by less than 2^-9."""
+E4M3 value to y = x / b, b = max fp32(1/448): half a step is 2^-4 |y|, below 2^-6
+the fixed 2^-10; the quotient, the constant and its product have a rounding
+each (3 u); a root raised to the smallest code is off by less than 2^-9."""
 import ctypes
 
 import numpy as np
@@ -197,6 +197,49 @@ def test_8bit_list_matches_formula(t, bf16, fresh):
         if d["b"] and d["b"][i]:
             assert torch.equal(d["b"][i].t, d["p"][i].t.to(torch.bfloat16))
     assert all(b.guard_intact() for k in d if d[k] for b in d[k] if b)
+
+
+def test_8bit_states_are_the_bits_of_their_definition():
+    """The states in fp32, every operation correctly rounded (numpy's are; a fused product is formed in float64, where
+    the product of two fp32 values is exact), and their codes: the same bits, the rare ones beside the middle of two
+    codes among them."""
+    n = 1 << 20
+    d = _lists8([n], 31, "none")
+    g, f = _f64(d["g"][0].t).astype(np.float32), np.float32
+    m0 = _restore(d["m"][0].t, d["ms"][0].t).astype(f)
+    r0 = _restore(d["v"][0].t, d["vs"][0].t).astype(f)
+    api.adamw8_multi_step(_tensors8(d), torch.full((1,), 77, dtype=torch.int64, device="cuda"), LR, (B1, B2), EPS, WD)
+    b1, b2, c1, c2 = f(B1), f(B2), f(1) - f(B1), f(1) - f(B2)
+    fma = lambda a, b, c: (a.astype(np.float64) * b + c).astype(f)  # noqa: E731
+    m = fma(g, c1, b1 * m0)
+    v = fma(g * g, c2, b2 * (r0 * r0))
+    for x, code, scale, root in ((m, "m", "ms", False), (np.sqrt(v), "v", "vs", True)):
+        x = _blocks(x)
+        b = np.abs(x).max(1) * (f(1) / f(448))
+        y = x / b[:, None]
+        if root:
+            y = np.where(x > 0, np.maximum(y, f(2.0 ** -9)), y)
+        want = torch.from_numpy(y.reshape(-1)[:n]).to(torch.float8_e4m3fn)
+        assert np.array_equal(d[scale][0].t.cpu().numpy(), b)
+        assert torch.equal(d[code][0].t.cpu().view(torch.uint8), want.view(torch.uint8))
+
+
+@pytest.mark.parametrize("top", [1e-30, 1e-36, 3e-38, 1e-41, 1e-44])
+def test_8bit_states_of_tiny_gradients(top):
+    """Blocks whose scale is subnormal or zero: m keeps the codes of its definition, or zeros."""
+    n, f = 512, np.float32
+    g = (np.linspace(-1, 1, n) * top).astype(f)
+    d = {k: torch.zeros(n, device="cuda") for k in ("p", "g")}
+    d["g"].copy_(torch.from_numpy(g))
+    m, ms, v, vs = api.adamw8_state(d["p"])
+    api.adamw8_multi_step(api.AdamW8Tensors([d["p"]], [d["g"]], [m], [ms], [v], [vs]),
+                          torch.ones(1, dtype=torch.int64, device="cuda"), LR, (B1, B2), EPS, WD)
+    x = _blocks(g * (f(1) - f(B1)))
+    b = np.abs(x).max(1) * (f(1) / f(448))
+    y = np.where(b[:, None] > 0, x / np.where(b > 0, b, f(1))[:, None], f(0))
+    assert np.array_equal(ms.cpu().numpy(), b)
+    assert torch.equal(m.cpu().float(), torch.from_numpy(y.reshape(-1)).clamp(-448, 448).to(torch.float8_e4m3fn).float())
+    assert torch.isfinite(v.float()).all() and torch.isfinite(d["p"]).all()
 
 
 def test_8bit_zero_gradients_and_states_only_decay():
