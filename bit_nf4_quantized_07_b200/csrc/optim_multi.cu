@@ -209,18 +209,26 @@ __device__ __forceinline__ void block_scale(float top, float &inv, float &b) {
     b = __fmul_rn(top, 1.0f / kE4m3Max);
     inv = b > 0.f ? __frcp_rn(b) : 0.f;
 }
-// Whether the code of |y| could depend on an error of 8 units in its last place: then its mantissa lies that near to the
-// middle between two codes, 0x80000 in the 20 bits below a code's three.  Codes below 2^-6 have the spacing of those
-// from 2^-6 to 2^-5.
-__device__ __forceinline__ bool near_middle(float y) {
-    float z = fabsf(y);
-    z = z < 0.015625f ? z + 0.015625f : z;
-    return ((__float_as_uint(z) + 0x80008u) & 0xfffffu) <= 16u;
+constexpr float kLess = 1.f - 0x1p-20f, kMore = 1.f + 0x1p-20f;
+__device__ __forceinline__ float least_root(float v) { return v > 0.f ? 0.001953125f : 0.f; }  // 2^-9, the smallest code
+
+// The codes of four elements by their definition; rarely called, and a call, so that it takes no registers of the others.
+__device__ __noinline__ uint2 codes_exact(float4 m, float4 v, float bm, float bv) {
+    const float x[8] = {m.x, m.y, m.z, m.w, v.x, v.y, v.z, v.w};
+    float y[4], z[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        y[k] = bm > 0.f ? __fdiv_rn(x[k], bm) : 0.f;
+        z[k] = fmaxf(bv > 0.f ? __fdiv_rn(__fsqrt_rn(x[4 + k]), bv) : 0.f, least_root(x[4 + k]));
+    }
+    return make_uint2(e4m3x4_pack(y), e4m3x4_pack(z));
 }
 
-// A warp takes one block per step and requests the next one's 2.5 KB before it
-// works on the present one's; a tensor's partial last block is read in its turn.
-constexpr int k8Ctas = 3;
+// A warp takes one block per step and requests the next two ones' 2.5 KB each
+// before it works on the present one's; a tensor's partial last block is read in
+// its turn.  448 tensors, 40 M elements: 157 us with two CTAs per SM; 162 us with
+// three and one block ahead, whose 80 registers spill.
+constexpr int k8Ctas = 2;
 
 template <int N>
 __global__ void __launch_bounds__(kMtThreads, k8Ctas)
@@ -236,10 +244,10 @@ adamw8_multi_kernel(const __grid_constant__ MtTable<qln_adamw8_tensor, N> T) {
         uint2 m, v;
         float bm, bv;
     };
-    Raw nxt;
+    Raw n1, n2;
     uint32_t ac = R.c;  // the look-ahead: its chunk and tensor
     int ati = R.ti;
-    auto request = [&]() {
+    auto request = [&](Raw &nxt) {
         if (ac < R.end) {
             while (ac >= T.chunk0[ati + 1]) ++ati;
             const qln_adamw8_tensor &t = T.t[ati];
@@ -259,14 +267,16 @@ adamw8_multi_kernel(const __grid_constant__ MtTable<qln_adamw8_tensor, N> T) {
         }
         ++ac;
     };
-    request();
+    request(n1);
+    request(n2);
     if (threadIdx.x == 0) sh = mt_step(T.a);
     __syncthreads();
     const MtStep S = sh;
     const float decay = 1.0f - T.a.lr * T.a.wd;
     for (; R.c < R.end; ++R.c) {
-        const Raw cur = nxt;
-        request();
+        const Raw cur = n1;
+        n1 = n2;
+        request(n2);
         while (R.c >= T.chunk0[R.ti + 1]) ++R.ti;
         const qln_adamw8_tensor &t = T.t[R.ti];
         const int64_t blk = (int64_t)(R.c - T.chunk0[R.ti]) * (kMtChunk / kBlock8) + warp;
@@ -334,46 +344,59 @@ adamw8_multi_kernel(const __grid_constant__ MtTable<qln_adamw8_tensor, N> T) {
         float im, iv, nm, nv;
         block_scale(__uint_as_float(am), im, nm);
         block_scale(__fsqrt_rn(__uint_as_float(av)), iv, nv);  // the largest root: the root is monotone
-        float ym[8], yv[8];
-        bool again = __float_as_uint(fmaxf(im, iv)) >= kInfBits;
+        // The codes of values 2^-20 smaller and 2^-20 larger: the errors of the root, of 1 / b and of the products (at
+        // most 5 units of 2^-24) lie within, so where both agree the value between them has that code.
+        const float im0 = __fmul_rn(im, kLess), im1 = __fmul_rn(im, kMore), iv0 = __fmul_rn(iv, kLess), iv1 = __fmul_rn(iv, kMore);
+        uint32_t mo[2], vo[2], diff = __float_as_uint(fmaxf(im1, iv1)) >= kInfBits;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            ym[k] = __fmul_rn(m[k], im);
-            yv[k] = __fmul_rn(root_approx(v[k]), iv);
-            again |= near_middle(ym[k]) | near_middle(yv[k]);
+        for (int h = 0; h < 2; ++h) {
+            float y0[4], y1[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                y0[k] = __fmul_rn(m[4 * h + k], im0);
+                y1[k] = __fmul_rn(m[4 * h + k], im1);
+            }
+            mo[h] = e4m3x4_pack(y0);
+            diff |= mo[h] ^ e4m3x4_pack(y1);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float x = root_approx(v[4 * h + k]), lo = least_root(v[4 * h + k]);
+                y0[k] = fmaxf(__fmul_rn(x, iv0), lo);
+                y1[k] = fmaxf(__fmul_rn(x, iv1), lo);
+            }
+            vo[h] = e4m3x4_pack(y0);
+            diff |= vo[h] ^ e4m3x4_pack(y1);
         }
-        if (__any_sync(0xffffffffu, again)) {
+        if (__any_sync(0xffffffffu, diff != 0)) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                ym[k] = nm > 0.f ? __fdiv_rn(m[k], nm) : 0.f;
-                yv[k] = nv > 0.f ? __fdiv_rn(__fsqrt_rn(v[k]), nv) : 0.f;
+            for (int h = 0; h < 2; ++h) {
+                const uint2 c = codes_exact(make_float4(m[4 * h], m[4 * h + 1], m[4 * h + 2], m[4 * h + 3]),
+                                            make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]), nm, nv);
+                mo[h] = c.x;
+                vo[h] = c.y;
             }
         }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) yv[k] = fmaxf(yv[k], v[k] > 0.f ? 0.001953125f : 0.f);  // 2^-9, the smallest code
         if (odd) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                if (abs_bits(m[k]) >= kInfBits) ym[k] = __uint_as_float(0x7fffffffu);
-                if (abs_bits(v[k]) >= kInfBits) yv[k] = __uint_as_float(0x7fffffffu);
+                if (abs_bits(m[k]) >= kInfBits) mo[k / 4] |= 0x7fu << (8 * (k % 4));
+                if (abs_bits(v[k]) >= kInfBits) vo[k / 4] |= 0x7fu << (8 * (k % 4));
             }
         }
-        const uint2 mo = make_uint2(e4m3x4_pack(ym), e4m3x4_pack(ym + 4));
-        const uint2 vo = make_uint2(e4m3x4_pack(yv), e4m3x4_pack(yv + 4));
         __syncwarp();  // every lane has read the scales
         if (lane == 0) {
             t.m_scale[blk] = nm;
             t.v_scale[blk] = nv;
         }
         if (whole) {
-            *reinterpret_cast<uint2 *>(t.m + e) = mo;
-            *reinterpret_cast<uint2 *>(t.v + e) = vo;
+            *reinterpret_cast<uint2 *>(t.m + e) = make_uint2(mo[0], mo[1]);
+            *reinterpret_cast<uint2 *>(t.v + e) = make_uint2(vo[0], vo[1]);
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 if (k < left) {
-                    t.m[e + k] = (uint8_t)((k < 4 ? mo.x : mo.y) >> (8 * (k & 3)));
-                    t.v[e + k] = (uint8_t)((k < 4 ? vo.x : vo.y) >> (8 * (k & 3)));
+                    t.m[e + k] = (uint8_t)(mo[k / 4] >> (8 * (k % 4)));
+                    t.v[e + k] = (uint8_t)(vo[k / 4] >> (8 * (k % 4)));
                 }
         }
     }
