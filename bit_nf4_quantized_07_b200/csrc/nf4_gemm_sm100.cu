@@ -69,11 +69,11 @@ struct Cfg {
     static_assert(MT * NT <= 2, "two TMEM accumulators of up to 256 columns at most");
     static constexpr int kStages = MT * NT == 1 ? 4 : 3;
     static constexpr int kMaxBN = NT == 1 ? 256 : 208;     // tokens per accumulator
-    // One decoder per 64-wide row block of the weight tile; MULTI: always 256, so that with MT = 1 two threads share a
-    // block.  That does not change a weight step (its chain of waits is longer than either decoding), but halves what a
-    // thread has to do in the steps of chunks (24 adapters in a tile: 22 us for them instead of 25).
+    // One decoder per 64-wide row block of the weight tile; MULTI: always 256, so that with MT = 1 there are two groups,
+    // which take the weight steps in turn: a step's chain of waits, decoding and fences is longer than its MMAs where
+    // there are few tokens, and two chains run side by side.  In the steps of chunks two threads share a row.
     static constexpr int kDecThreads = MULTI ? 256 : 128 * MT;
-    static constexpr int kShare = kDecThreads / (128 * MT);  // threads per block
+    static constexpr int kShare = kDecThreads / (128 * MT);  // groups, or threads per row of a chunk
     static constexpr int kThreads = 64 + kDecThreads;
     static constexpr uint32_t kABytes = 16384u * MT;        // MT x (128 rows x 64 K) bf16
     static constexpr uint32_t kBBytes = NT * kMaxBN * kBK * 2;
@@ -537,7 +537,7 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
             }
             return r;
         };
-        Raw r0 = fetch(0), r1 = fetch(1);
+        Raw r0 = fetch(share), r1 = fetch(share + C::kShare);
         // This thread's 32 code bytes sit at a 32-byte stride; the two 16-byte
         // halves are read in an order that keeps each 8-thread phase on
         // distinct banks (half `cfirst` first).
@@ -552,12 +552,14 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
         // holds chunks 4*cfirst.. , folded into the XOR base as well.
         const uint32_t row_off = (TRANS ? dcol * 8192 : 0) + (drow >> 3) * 1024 + r8 * 128;
         const uint32_t sA0 = smem_addr(smem + C::kOffA) + row_off + (r8 << 4);
-        for (int kt = 0; kt < nsteps; ++kt) {
+        // A group that takes every second step leaves out phases of the barriers; it never falls two behind one, since the
+        // MMAs end in their order and it has waited for one of the last S + 2 steps.
+        for (int kt = share; kt < nsteps; kt += C::kShare) {
             const int s = kt % S;
             const uint32_t ph = (uint32_t)(kt / S) & 1u;
             const float ah = p.qabs ? dq_restore((uint32_t)r0.q, r0.v, mu, p.e4m3) : r0.v;
             r0 = r1;
-            r1 = fetch(kt + 2);
+            r1 = fetch(kt + 2 * C::kShare);
             if (!mbar_wait_bounded(empty(s), ph ^ 1u, abort_flag, kWaitLimitNs)) {
                 give_up();
                 break;
@@ -568,33 +570,22 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                     break;
                 }
                 const uint8_t *cptr = smem + C::kOffC + s * C::kCBytes + code_off;
-                if constexpr (C::kShare == 1) {
-                    const uint4 ca = *reinterpret_cast<const uint4 *>(cptr + 16 * cfirst);
-                    const uint4 cb = *reinterpret_cast<const uint4 *>(cptr + 16 * (cfirst ^ 1));
-                    const NF4Table tab = nf4_table(ah);
-                    const uint32_t xa = (sA0 + s * C::kABytes) ^ (cfirst << 6);  // chunks of ca: 4*cfirst + i
-                    const uint32_t xb = xa ^ 64u;                                  // chunks of cb
-                    st_shared_v4(xa ^ 0u, nf4_decode8(ca.x, tab));
-                    st_shared_v4(xa ^ 16u, nf4_decode8(ca.y, tab));
-                    st_shared_v4(xa ^ 32u, nf4_decode8(ca.z, tab));
-                    st_shared_v4(xa ^ 48u, nf4_decode8(ca.w, tab));
-                    st_shared_v4(xb ^ 0u, nf4_decode8(cb.x, tab));
-                    st_shared_v4(xb ^ 16u, nf4_decode8(cb.y, tab));
-                    st_shared_v4(xb ^ 32u, nf4_decode8(cb.z, tab));
-                    st_shared_v4(xb ^ 48u, nf4_decode8(cb.w, tab));
-                } else {  // half of the block: the one read first or second above
-                    const uint32_t half = cfirst ^ (uint32_t)share;
-                    const uint4 ca = *reinterpret_cast<const uint4 *>(cptr + 16 * half);
-                    const NF4Table tab = nf4_table(ah);
-                    const uint32_t xa = (sA0 + s * C::kABytes) ^ (half << 6);
-                    st_shared_v4(xa ^ 0u, nf4_decode8(ca.x, tab));
-                    st_shared_v4(xa ^ 16u, nf4_decode8(ca.y, tab));
-                    st_shared_v4(xa ^ 32u, nf4_decode8(ca.z, tab));
-                    st_shared_v4(xa ^ 48u, nf4_decode8(ca.w, tab));
-                }
+                const uint4 ca = *reinterpret_cast<const uint4 *>(cptr + 16 * cfirst);
+                const uint4 cb = *reinterpret_cast<const uint4 *>(cptr + 16 * (cfirst ^ 1));
+                const NF4Table tab = nf4_table(ah);
+                const uint32_t xa = (sA0 + s * C::kABytes) ^ (cfirst << 6);  // chunks of ca: 4*cfirst + i
+                const uint32_t xb = xa ^ 64u;                                  // chunks of cb
+                st_shared_v4(xa ^ 0u, nf4_decode8(ca.x, tab));
+                st_shared_v4(xa ^ 16u, nf4_decode8(ca.y, tab));
+                st_shared_v4(xa ^ 32u, nf4_decode8(ca.z, tab));
+                st_shared_v4(xa ^ 48u, nf4_decode8(ca.w, tab));
+                st_shared_v4(xb ^ 0u, nf4_decode8(cb.x, tab));
+                st_shared_v4(xb ^ 16u, nf4_decode8(cb.y, tab));
+                st_shared_v4(xb ^ 32u, nf4_decode8(cb.z, tab));
+                st_shared_v4(xb ^ 48u, nf4_decode8(cb.w, tab));
                 fence_proxy_async_smem();
             }
-            mbar_arrive(dec_full(s));
+            mbar_arrive_n(dec_full(s), C::kShare);
         }
         if constexpr (MULTI) {
             if (!*abort_flag && !mbar_wait_bounded(list_full, 0, abort_flag, kWaitLimitNs)) give_up();
