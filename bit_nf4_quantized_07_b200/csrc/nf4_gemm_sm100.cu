@@ -72,7 +72,7 @@ struct Cfg {
     // One decoder per 64-wide row block of the weight tile; MULTI: always 256, so that with MT = 1 there are two groups,
     // which take the weight steps in turn: a step's chain of waits, decoding and fences is longer than its MMAs where
     // there are few tokens, and two chains run side by side.  In the steps of chunks two threads share a row.
-    static constexpr int kDecThreads = MULTI ? 256 : 128 * MT;
+    static constexpr int kDecThreads = MULTI ? 256 * MT : 128 * MT;
     static constexpr int kShare = kDecThreads / (128 * MT);  // groups, or threads per row of a chunk
     static constexpr int kThreads = 64 + kDecThreads;
     static constexpr uint32_t kABytes = 16384u * MT;        // MT x (128 rows x 64 K) bf16
@@ -781,8 +781,8 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
         if (*epi_go && ks == 1) {
             tc_fence_after();
             const int q = warp & 3;              // TMEM lane quadrant of this warp
-            const int sub = C::kShare == 1 ? (warp - 2) >> 2 : 0;   // weight sub-tile of this warp
-            const int part = C::kShare == 1 ? 0 : (warp - 2) >> 2;  // or which of the two warps of a quadrant it is
+            const int sub = MT == 2 ? ((warp - 2) >> 2) & 1 : 0;    // weight sub-tile of this warp
+            const int part = ((warp - 2) >> 2) / MT;                // which of the warps of its quadrant it is
             uint16_t *Os = reinterpret_cast<uint16_t *>(smem);  // [NT*BN][TM] bf16; all MMAs are done
             const int m = sub * kBM + q * 32 + lane;
 #pragma unroll
@@ -840,7 +840,7 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                 // Eight columns at a time in a short loop: this code runs once, and unrolled over 32 columns its
                 // instructions took longer to fetch (8 us) than its data to move.
                 tc_fence_after();
-                const int q = warp & 3, sub = C::kShare == 1 ? (warp - 2) >> 2 : 0, part = C::kShare == 1 ? 0 : (warp - 2) >> 2;
+                const int q = warp & 3, sub = MT == 2 ? ((warp - 2) >> 2) & 1 : 0, part = ((warp - 2) >> 2) / MT;
                 const uint32_t mine = sbase + (uint32_t)((kz * cq) * TM + sub * kBM + q * 32 + lane) * 4u;
 #pragma unroll 1
                 for (int col = 8 * part; col < ntok; col += 8 * C::kShare) {
