@@ -989,10 +989,12 @@ static TileShape choose_shape(int64_t M, int64_t K, int64_t n, int num_sms) {
     return best;
 }
 
-// Tile shape and K split of a MULTI call.  A k-step takes 1200 cycles at least (its chain of copy, decoding and MMA
-// through the ring; 1600 with MT = 2), and 1.25 (1.35) times its tensor time where that is more; a tile takes 4000
-// cycles besides, and a split 6000 more for the exchange.  Splitting fills the SMs where there are few tiles:
-// 4096 x 4096 and 333 tokens, rank 8: 37 us split in four, 58 us unsplit; 64 tokens: 28 us and 54 us.
+// Tile shape and K split of a MULTI call, by a cost in cycles that was fitted to 274 measured calls (13 sizes, every shape;
+// it meets them within 5 % and its choices are within 2 % of the best).  A k-step takes its chain of copy, decoding and
+// MMA through the ring plus 0.18 of its tensor time, or the tensor time where that is more; a tile its start and, per
+// column, its epilogue; a split the exchange, and in four slower steps besides.  CTAs of clusters find fewer places.
+// Splitting fills the SMs where there are few tiles: 4096 x 4096 and 64 tokens, rank 16: 21 us split in three, 37 us
+// unsplit; 333 tokens: 33 us split in two, 40 us unsplit.
 struct MultiShape {
     TileShape t;
     int ks;
@@ -1013,12 +1015,12 @@ static MultiShape choose_multi(int64_t M, int64_t K, int64_t n, int num_sms) {
                 // the exchange takes the stages' shared memory
                 const int64_t room = MT * NT == 2 ? Cfg<2, 1, true>::kOffBar : Cfg<1, 1, true>::kOffBar;
                 if (ks > 1 && (ks * 4 > KT || (int64_t)ks * split_cols((int)tok, ks) * kBM * MT * 4 > room)) continue;
-                // CTAs that run at once: a cluster stays within one of 8 groups of about 18 SMs
-                const int64_t slots = ks == 1 ? num_sms : (int64_t)8 * (18 / ks) * ks;
-                const int64_t rounds = (tiles * ks + slots - 1) / slots;
-                const double mma = (MT == 2 ? 1.35 : 1.25) * 2.0 * kBM * MT * (double)tok * kBK / 5700.0;
-                const double least = MT == 2 ? 1600.0 : 1200.0;
-                const double cost = rounds * (((KT + ks - 1) / ks + 1) * ((mma > least ? mma : least) + 0.15 * mma) + 4000.0 + (ks > 1 ? 6000.0 : 0.0)) *
+                const int64_t places[5] = {0, num_sms, num_sms - 4, num_sms - 10, num_sms - 20};
+                const int64_t rounds = (tiles * ks + places[ks] - 1) / places[ks];
+                const double mma = 2.0 * kBM * MT * (double)tok * kBK / 5700.0;
+                const double chain = (MT == 2 ? 1270.0 : NT == 2 ? 970.0 : 750.0) + 0.18 * mma;
+                const double step = (chain > 1.05 * mma ? chain : 1.05 * mma) * (ks == 4 ? 1.2 : 1.0);
+                const double cost = rounds * (((KT + ks - 1) / ks + 1) * step + 3350.0 + 43.0 * MT * (double)tok + (ks > 1 ? 5400.0 : 0.0)) *
                                     (1.0 + 1e-4 * (double)(ttiles * tok - n) / (double)n);
                 if (cost < best_cost * 0.999) {
                     best_cost = cost;
