@@ -141,7 +141,7 @@ MultiWs multi_layout(bool bwd, int64_t n, int r) {
 }
 
 constexpr int64_t kMaxMultiTokens = (int64_t)1 << 24;
-constexpr int64_t kMaxStreamWeights = (int64_t)24 << 20;
+constexpr int64_t kMaxStreamWeights = (int64_t)16 << 20;
 
 qln_status check_multi(const qln_nf4_weight *w, const qln_adapter_pool *pool, const uint16_t *X, int64_t n,
                        const int32_t *ids) {
@@ -483,10 +483,12 @@ qln_status qlora_multi_fwd(const qln_nf4_weight *w, const qln_adapter_pool *pool
         e = qln::launch_adapter_down_small(X, n, w->cols, pool, ids, U_out, sU, status, cs);
         if (e != cudaSuccess) return QLN_ERR_CUDA;
         // The weight stream, whose shared-memory and instruction cost per weight grows with every 8 tokens, or the
-        // GEMM with its K split, about 17 us and 0.42 us per million weights whatever n.  Measured (us, stream / GEMM),
-        // rank 16 to 64: 4096 x 4096 n = 8: 14 / 24, 16: 17 / 24, 24: 20 / 25, 32: 30 / 27; 8192 x 8192 n = 8: 32 / 44,
-        // 16: 50 / 45, 30: 84 / 46; 4096 x 11008 n = 12: 40 / 35, 24: 57 / 40; 11008 x 4096 n = 16: 30 / 32.
-        const bool streams = n <= 8 || (n <= 24 && w->rows * w->cols <= kMaxStreamWeights);
+        // GEMM with its K split, whose time hardly depends on n, but on the ranks of all the tile's adapters.  Measured
+        // (us, stream / GEMM, an adapter per token): rank 16: 4096 x 4096 n = 1: 12.8 / 15.0, 8: 13.5 / 15.7, 16: 16.7 /
+        // 16.5, 24: 19.8 / 17.6; 8192 x 8192 n = 8: 28 / 40, 12: 49 / 40; 4096 x 11008 n = 8: 22 / 31, 12: 39 / 32.
+        // Rank 64: 2048 x 2048 n = 16: 15.1 / 16.4; 4096 x 4096 n = 16: 21.9 / 21.0, 24: 26.9 / 29.8; 5120 x 5120
+        // n = 24: 40 / 38.
+        const bool streams = n <= 8 || (n <= 24 && pool->r > 32 && w->rows * w->cols <= kMaxStreamWeights);
         if (streams && qln::nf4_decode_fwd_supported(w, n, pool->r, true))
             return from_cuda(qln::launch_nf4_decode_fwd_multi(w, X, n, sU, pool, ids, Y, status, cs));
         return from_cuda(multi_gemm(w, false, X, n, sU, pool->B, pool, ids, Y, status, cs, sms));
