@@ -1011,12 +1011,15 @@ static MultiShape choose_multi(int64_t M, int64_t K, int64_t n, int num_sms) {
         for (int bn = NT == 1 ? 256 : 208; bn >= 16; bn -= 16) {
             if (bn < 128 && (int64_t)NT * bn < n) break;  // narrow tiles only for small n
             const int64_t tok = (int64_t)NT * bn, ttiles = (n + tok - 1) / tok, tiles = ttiles * (M / (kBM * MT));
+            const int64_t less = tok - 16 * NT;  // the next narrower tile, better if as many of them cover the tokens
+            if (bn > 16 && (bn > 128 || less >= n) && (n + less - 1) / less == ttiles) continue;
             for (int ks = 1; ks <= 4; ++ks) {
                 // the exchange takes the stages' shared memory
                 const int64_t room = MT * NT == 2 ? Cfg<2, 1, true>::kOffBar : Cfg<1, 1, true>::kOffBar;
                 if (ks > 1 && (ks * 4 > KT || (int64_t)ks * split_cols((int)tok, ks) * kBM * MT * 4 > room)) continue;
-                const int64_t places[5] = {0, num_sms, num_sms - 4, num_sms - 10, num_sms - 20};
-                const int64_t rounds = (tiles * ks + places[ks] - 1) / places[ks];
+                const int lost[5] = {0, 0, 4, 10, 20};
+                const int64_t places = num_sms > lost[ks] + ks ? num_sms - lost[ks] : ks;
+                const int64_t rounds = (tiles * ks + places - 1) / places;
                 const double mma = 2.0 * kBM * MT * (double)tok * kBK / 5700.0;
                 const double chain = (MT == 2 ? 1270.0 : NT == 2 ? 970.0 : 750.0) + 0.18 * mma;
                 const double step = (chain > 1.05 * mma ? chain : 1.05 * mma) * (ks == 4 ? 1.2 : 1.0);
