@@ -172,15 +172,23 @@ __device__ __forceinline__ float ad_peer_f32(uint32_t saddr, uint32_t rank) {
 }
 
 // v as a sum of three bf16 values (24 bits of mantissa, what v holds): the
-// operand of the fp32 gradients.  What a non-finite v leaves is dropped, so
-// that an infinity stays one.
+// operand of the fp32 gradients.  All three have v's sign and none is zero
+// unless v is (or below 2^-100, where the last ones underflow): an infinite
+// element of dY or X times v is then the infinity of their product, where a zero
+// part would make it NaN and parts of both signs would cancel.  So each part is
+// cut off towards zero and, if that leaves nothing, lowered by one unit.  An
+// infinity or NaN is all three.
 __device__ __forceinline__ void split3(float v, uint16_t (&q)[3]) {
+    if (!isfinite(v)) {
+        q[0] = q[1] = q[2] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+        return;
+    }
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-        const __nv_bfloat16 h = __float2bfloat16_rn(v);
-        q[k] = __bfloat16_as_ushort(h);
-        v = __fsub_rn(v, __bfloat162float(h));
-        if (!isfinite(v)) v = 0.f;
+        uint32_t h = __float_as_uint(v) & 0xffff0000u;
+        if (k < 2 && h == __float_as_uint(v) && (h << 1) != 0u) h -= 0x10000u;
+        q[k] = (uint16_t)(h >> 16);
+        v = __fsub_rn(v, __uint_as_float(h));
     }
 }
 

@@ -415,7 +415,9 @@ QLN_API qln_status qlora_multi_fwd(const qln_nf4_weight *w, const qln_adapter_po
  * past an adapter's rank.  Sums run in an order fixed by the sizes and ids.
  * U (nullable) is U_out of the matching forward; when NULL it is recomputed.
  * G and U enter dA and dB as the fp32 values they are (three bf16 parts, whose
- * products with X and dY are exact), with fp32 accumulation.
+ * products with X and dY are exact), with fp32 accumulation.  An infinite
+ * element of X or dY gives the elements of its own adapter's dA or dB that it
+ * enters the infinity or NaN of the formula (G and U below 2^-100 may give NaN).
  * ws: at least qln_workspace_bytes(QLN_OP_MULTI_BWD, dout, din, n, r) bytes.
  * Errors: as qlora_multi_fwd, for dY, dX, dA and dB too.
  */
