@@ -579,24 +579,24 @@ static cudaError_t launch_cluster(void (*kernel)(const Args), dim3 grid, dim3 cl
 }
 
 template <int NT, bool WKM>
-static cudaError_t launch_ad_down(const DownArgs &a, cudaStream_t st) {
+static cudaError_t launch_ad_down(const DownArgs &a, cudaStream_t st, int num_sms) {
     constexpr size_t smem = (size_t)kAdStages * (64 * kAdLd + (WKM ? 64 * (NT * 8 + 8) : NT * 8 * kAdLd)) * sizeof(uint16_t);
     static_assert(smem >= 64 * (NT * 8 + 4) * 4, "the partial tile fits into the ring");
     // every group's last tile may be partial: at most n / 64 whole tiles and one more per group present
     const int64_t tiles = a.n / 64 + (a.count + 1 < a.n ? a.count + 1 : a.n);
     // Eight CTAs per tile while all fit at once, for the shortest chain (4096 columns, 100 tokens of 8 adapters: 27.3 us
     // for the whole call, 29.4 us with four), else four (28672 columns, rank 64, 4096 tokens: 99 us against 115).
-    const int64_t slots = 148 * ((int64_t)(228 * 1024) / (int64_t)(smem + 1024));
+    const int64_t slots = num_sms * ((int64_t)(228 * 1024) / (int64_t)(smem + 1024));
     const unsigned cl = tiles * kAdCluster <= slots ? kAdCluster : kAdCluster / 2;
     return launch_cluster(adapter_down_kernel<NT, WKM>, dim3((unsigned)tiles, cl), dim3(1, cl), smem, st, a);
 }
 
 cudaError_t launch_adapter_down(const uint16_t *in, int64_t n, int64_t K, const qln_adapter_pool *pool, bool kmajor,
                                 const AdapterPlan &p, float *full, uint16_t *scaled, uint16_t *split, const float *aux,
-                                uint16_t *aux_split, cudaStream_t st) {
+                                uint16_t *aux_split, cudaStream_t st, int num_sms) {
     const DownArgs a{in, kmajor ? pool->B : pool->A, n, K, pool->r, pool->count, p.order, p.start, p.tiles, pool->rank,
                      pool->scale, full, scaled, split, aux, aux_split};
-#define QLN_AD_DOWN(NT) (kmajor ? launch_ad_down<NT, true>(a, st) : launch_ad_down<NT, false>(a, st))
+#define QLN_AD_DOWN(NT) (kmajor ? launch_ad_down<NT, true>(a, st, num_sms) : launch_ad_down<NT, false>(a, st, num_sms))
     if (a.r <= 8) return QLN_AD_DOWN(1);
     if (a.r <= 16) return QLN_AD_DOWN(2);
     if (a.r <= 32) return QLN_AD_DOWN(4);
@@ -606,13 +606,14 @@ cudaError_t launch_adapter_down(const uint16_t *in, int64_t n, int64_t K, const 
 }
 
 cudaError_t launch_adapter_down_small(const uint16_t *in, int64_t n, int64_t K, const qln_adapter_pool *pool,
-                                      const int32_t *ids, float *full, uint16_t *scaled, int *status, cudaStream_t st) {
+                                      const int32_t *ids, float *full, uint16_t *scaled, int *status, cudaStream_t st,
+                                      int num_sms) {
     const SmallArgs a{in, pool->A, (int)n, pool->r, pool->count, K, ids, pool->rank, pool->scale, full, scaled, status};
     const unsigned groups = (unsigned)(n < pool->count ? n : pool->count), jt = (unsigned)((pool->r + 15) / 16);
     // Clusters of 8 for the shortest chain; of 4 where those would put two CTAs on an SM (whole calls of 4096 x 4096, 8 / 4:
     // one token 12.6 / 13.2 us; 32 tokens of 32 adapters, rank 16: 25.9 / 22.7 us, rank 64: 41 / 38 us).
 #define QLN_AD_SMALL(NT) \
-    (groups * jt * 8 <= 148 ? launch_cluster(adapter_down_small_kernel<NT, 8>, dim3(groups, jt, 8), dim3(1, 1, 8), 0, st, a) \
+    (groups * jt * 8 <= (unsigned)num_sms ? launch_cluster(adapter_down_small_kernel<NT, 8>, dim3(groups, jt, 8), dim3(1, 1, 8), 0, st, a) \
                             : launch_cluster(adapter_down_small_kernel<NT, 4>, dim3(groups, jt, 4), dim3(1, 1, 4), 0, st, a))
     switch ((n + 7) / 8) {
         case 1: return QLN_AD_SMALL(1);

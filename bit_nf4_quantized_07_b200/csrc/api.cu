@@ -480,7 +480,7 @@ qln_status qlora_multi_fwd(const qln_nf4_weight *w, const qln_adapter_pool *pool
     int *status = reinterpret_cast<int *>(wsb);
     cudaError_t e;
     if (n <= 32) {  // one warp holds all ids: no plan
-        e = qln::launch_adapter_down_small(X, n, w->cols, pool, ids, U_out, sU, status, cs);
+        e = qln::launch_adapter_down_small(X, n, w->cols, pool, ids, U_out, sU, status, cs, sms);
         if (e != cudaSuccess) return QLN_ERR_CUDA;
         // The weight stream, whose shared-memory and instruction cost per weight grows with every 8 tokens, or the
         // GEMM with its K split, whose time hardly depends on n, but on the ranks of all the tile's adapters.  Measured
@@ -495,7 +495,7 @@ qln_status qlora_multi_fwd(const qln_nf4_weight *w, const qln_adapter_pool *pool
     }
     e = qln::launch_adapter_plan(ids, n, pool->count, plan, status, cs);
     if (e != cudaSuccess) return QLN_ERR_CUDA;
-    e = qln::launch_adapter_down(X, n, w->cols, pool, false, plan, U_out, sU, nullptr, nullptr, nullptr, cs);
+    e = qln::launch_adapter_down(X, n, w->cols, pool, false, plan, U_out, sU, nullptr, nullptr, nullptr, cs, sms);
     if (e != cudaSuccess) return QLN_ERR_CUDA;
     return from_cuda(multi_gemm(w, false, X, n, sU, pool->B, pool, ids, Y, status, cs, sms));
 }
@@ -523,10 +523,10 @@ qln_status qlora_multi_bwd(const qln_nf4_weight *w, const qln_adapter_pool *pool
     cudaError_t e = qln::launch_adapter_plan(ids, n, pool->count, plan, status, cs);
     if (e != cudaSuccess) return QLN_ERR_CUDA;
     if (!U) {
-        e = qln::launch_adapter_down(X, n, w->cols, pool, false, plan, nullptr, nullptr, U3, nullptr, nullptr, cs);
+        e = qln::launch_adapter_down(X, n, w->cols, pool, false, plan, nullptr, nullptr, U3, nullptr, nullptr, cs, sms);
         if (e != cudaSuccess) return QLN_ERR_CUDA;
     }
-    e = qln::launch_adapter_down(dY, n, w->rows, pool, true, plan, nullptr, sG, G3, U, U ? U3 : nullptr, cs);
+    e = qln::launch_adapter_down(dY, n, w->rows, pool, true, plan, nullptr, sG, G3, U, U ? U3 : nullptr, cs, sms);
     if (e != cudaSuccess) return QLN_ERR_CUDA;
     e = qln::launch_adapter_grads(dY, U3, w->rows, X, G3, w->cols, n, pool, plan, dA, dB, status, cs, sms);
     if (e != cudaSuccess) return QLN_ERR_CUDA;

@@ -112,10 +112,11 @@ cudaError_t launch_adapter_plan(const int32_t *ids, int64_t n, int count, const 
 // (each may be null); with aux_split also the planes of aux (fp32 [n][r])
 cudaError_t launch_adapter_down(const uint16_t *in, int64_t n, int64_t K, const qln_adapter_pool *pool, bool kmajor,
                                 const AdapterPlan &p, float *full, uint16_t *scaled, uint16_t *split, const float *aux,
-                                uint16_t *aux_split, cudaStream_t st);
+                                uint16_t *aux_split, cudaStream_t st, int num_sms);
 // the same for n <= 32 without a plan, A only (full may be null; columns past a rank are zero in both)
 cudaError_t launch_adapter_down_small(const uint16_t *in, int64_t n, int64_t K, const qln_adapter_pool *pool,
-                                      const int32_t *ids, float *full, uint16_t *scaled, int *status, cudaStream_t st);
+                                      const int32_t *ids, float *full, uint16_t *scaled, int *status, cudaStream_t st,
+                                      int num_sms);
 // adapter_grads.cu: dA and dB of every adapter; U3, G3: three bf16 planes of n * r
 cudaError_t launch_adapter_grads(const uint16_t *dY, const uint16_t *U3, int64_t dout, const uint16_t *X,
                                  const uint16_t *G3, int64_t din, int64_t n, const qln_adapter_pool *pool,
