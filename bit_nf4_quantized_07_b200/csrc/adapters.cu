@@ -612,9 +612,10 @@ cudaError_t launch_adapter_down_small(const uint16_t *in, int64_t n, int64_t K, 
     const unsigned groups = (unsigned)(n < pool->count ? n : pool->count), jt = (unsigned)((pool->r + 15) / 16);
     // Clusters of 8 for the shortest chain; of 4 where those would put two CTAs on an SM (whole calls of 4096 x 4096, 8 / 4:
     // one token 12.6 / 13.2 us; 32 tokens of 32 adapters, rank 16: 25.9 / 22.7 us, rank 64: 41 / 38 us).
+    const bool eight = groups * jt * 8 <= (unsigned)num_sms;
 #define QLN_AD_SMALL(NT) \
-    (groups * jt * 8 <= (unsigned)num_sms ? launch_cluster(adapter_down_small_kernel<NT, 8>, dim3(groups, jt, 8), dim3(1, 1, 8), 0, st, a) \
-                            : launch_cluster(adapter_down_small_kernel<NT, 4>, dim3(groups, jt, 4), dim3(1, 1, 4), 0, st, a))
+    (eight ? launch_cluster(adapter_down_small_kernel<NT, 8>, dim3(groups, jt, 8), dim3(1, 1, 8), 0, st, a) \
+           : launch_cluster(adapter_down_small_kernel<NT, 4>, dim3(groups, jt, 4), dim3(1, 1, 4), 0, st, a))
     switch ((n + 7) / 8) {
         case 1: return QLN_AD_SMALL(1);
         case 2: return QLN_AD_SMALL(2);

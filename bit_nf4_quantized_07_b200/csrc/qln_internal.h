@@ -124,7 +124,7 @@ cudaError_t launch_adapter_grads(const uint16_t *dY, const uint16_t *U3, int64_t
                                  int num_sms);
 
 // The adapters of a GEMM over tokens with adapters of their own: lact is
-// bf16(s U) [n][r] and lw the pool's factor base, `stride` elements per adapter.
+// bf16(s U) [n][r] and lw the pool's factors, A or B.
 struct AdapterView {
     const int32_t *ids, *rank;
     int count;

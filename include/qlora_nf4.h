@@ -387,7 +387,11 @@ typedef struct {
  * a = ids[t], and none (only X W'^T) if a is outside 0 .. count - 1.
  *   X [n][din] bf16 in; ids [n] int32 in (device), in any order;
  *   Y [n][dout] bf16 out = bf16_RN(X_t W'^T + s_a (X_t A_a^T) B_a^T), fp32
- *   accumulation, with bf16(s_a U_t) as the tensor cores' operand;
+ *   accumulation, with bf16(s_a U_t) as the tensor cores' operand.  Up to 24
+ *   tokens may go by a weight stream, which does not round W' to bf16: it
+ *   multiplies X with the book's entries as bf16 and scales each block's fp32
+ *   partial sum by ahat.  Its Y is 2.5e-3 of the norm off the value on W', where
+ *   the rounding of Y alone is 1.7e-3;
  *   U_out [n][r] fp32 out (nullable): U_t = X_t A_a^T, unscaled, zero past the
  *   adapter's rank and for tokens without one, for reuse by qlora_multi_bwd.
  * A token's row of Y and U depends on its own row of X and its own adapter
