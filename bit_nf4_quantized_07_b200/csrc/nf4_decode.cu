@@ -137,7 +137,6 @@ __device__ __forceinline__ void df_mma_zero(float (&d)[4], const uint32_t (&a)[4
 // best, with 0.63e-3 (largest single error 1.93e-3 instead of 3.1e-3).
 constexpr float kDfGamma = 1.437006f;
 
-constexpr int64_t kDfMultiTokens = 24;  // tokens of a MULTI call, at most: more always take the GEMM
 constexpr int kDfPairs = 4;  // (tile, adapter) pairs of a warp whose first B fragment is loaded ahead
 
 template <int NT, bool MULTI>  // token tiles of 8: n <= 8 * NT
@@ -173,8 +172,8 @@ nf4_decode_fwd_kernel(const __grid_constant__ CUtensorMap tm_codes, const DfPara
     const uint32_t slots_s = smem_u32(dsm + p.off_slots), uslots_s = smem_u32(dsm + p.off_uslots);
     const int ahs = nkbx + 1;
     const int xs = MULTI ? p.xs : 256, x0 = MULTI ? p.off_x : 128;  // X lines
-    __shared__ int s_gid[MULTI ? 8 * NT : 1];         // the tokens' adapters, each once; -1 for tokens without one
-    __shared__ uint32_t s_gmask[MULTI ? 8 * NT : 1];  // their tokens
+    __shared__ int s_gid[MULTI ? 33 : 1];         // the tokens' adapters, each once; -1 for tokens without one
+    __shared__ uint32_t s_gmask[MULTI ? 33 : 1];  // their tokens
     __shared__ int s_groups;
 
     // Before the dependency wait only shared memory and the launch's own
@@ -287,7 +286,8 @@ nf4_decode_fwd_kernel(const __grid_constant__ CUtensorMap tm_codes, const DfPara
         if (warp == 0) {  // the batch's groups
             const int id = lane < n ? __ldg(p.ids + lane) : 0;
             const int a = (unsigned)id < (unsigned)p.count ? id : -1;
-            const uint32_t same = __match_any_sync(0xffffffffu, lane < n ? a : -2) & ((1u << n) - 1u);
+            const uint32_t live = n == 32 ? 0xffffffffu : (1u << n) - 1u;
+            const uint32_t same = __match_any_sync(0xffffffffu, lane < n ? a : -2) & live;
             const bool lead = lane < n && (same & ((1u << lane) - 1u)) == 0;
             const uint32_t leads = __ballot_sync(0xffffffffu, lead);
             if (lead) {
@@ -736,7 +736,7 @@ static bool df_plan_s(int64_t T, int64_t KB, int r, int NT, int S, int64_t Q, bo
 }
 
 bool nf4_decode_fwd_supported(const qln_nf4_weight *w, int64_t n, int r, bool multi) {
-    if (n < 1 || n > (multi ? kDfMultiTokens : 32) || (w->rows % 16) != 0 || (w->cols % 64) != 0 || (r % 8) != 0 || r < 8 || r > 128)
+    if (n < 1 || n > 32 || (w->rows % 16) != 0 || (w->cols % 64) != 0 || (r % 8) != 0 || r < 8 || r > 128)
         return false;
     // the kernel's index arithmetic is 32-bit: block indices and tile counts times the grid must fit
     if (w->rows * (w->cols / 64) >= ((int64_t)1 << 31) || (w->rows / 16) * 1024 >= ((int64_t)1 << 31)) return false;
@@ -880,9 +880,7 @@ static cudaError_t launch_df_nt(const DfParams &p, const qln_nf4_weight *w, cuda
         case 1: return launch_df<1, MULTI>(p, w, st);
         case 2: return launch_df<2, MULTI>(p, w, st);
         case 3: return launch_df<3, MULTI>(p, w, st);
-        default:
-            if constexpr (MULTI) return cudaErrorInvalidValue;  // more than kDfMultiTokens
-            else return launch_df<4, false>(p, w, st);
+        default: return launch_df<4, MULTI>(p, w, st);
     }
 }
 
