@@ -487,8 +487,12 @@ qln_status qlora_multi_fwd(const qln_nf4_weight *w, const qln_adapter_pool *pool
         // (us, stream / GEMM, an adapter per token): rank 16: 4096 x 4096 n = 1: 12.8 / 15.0, 8: 13.5 / 15.7, 16: 16.7 /
         // 16.5, 24: 19.8 / 17.6; 8192 x 8192 n = 8: 28 / 40, 12: 49 / 40; 4096 x 11008 n = 8: 22 / 31, 12: 39 / 32.
         // Rank 64: 2048 x 2048 n = 16: 15.1 / 16.4; 4096 x 4096 n = 16: 21.9 / 21.0, 24: 26.9 / 29.8; 5120 x 5120
-        // n = 24: 40 / 38.
-        const bool streams = n <= 8 || (n <= 24 && pool->r > 32 && w->rows * w->cols <= kMaxStreamWeights);
+        // n = 24: 40 / 38.  Over several epochs (back to back): 28672 x 8192 n = 1: 71 / 115, 8: 81 / 119; 8192 x 28672
+        // n = 1: 97 / 114, 8: 113 / 126.  Where rows are not a multiple of 128 the other side is the register-level GEMM:
+        // 1088 x 2048 n = 24: 15 / 52; 4160 x 4096 n = 9: 17 / 60, 16: 19 / 102, 32: 38 / 122; 28736 x 8192, rank 64,
+        // n = 32: 311 / 351.
+        const bool streams = n <= 8 || !qln::nf4_tc_gemm_multi_supported(w, false, pool->r) ||
+                             (n <= 24 && pool->r > 32 && w->rows * w->cols <= kMaxStreamWeights);
         if (streams && qln::nf4_decode_fwd_supported(w, n, pool->r, true))
             return from_cuda(qln::launch_nf4_decode_fwd_multi(w, X, n, sU, pool, ids, Y, status, cs));
         return from_cuda(multi_gemm(w, false, X, n, sU, pool->B, pool, ids, Y, status, cs, sms));

@@ -387,7 +387,7 @@ typedef struct {
  * a = ids[t], and none (only X W'^T) if a is outside 0 .. count - 1.
  *   X [n][din] bf16 in; ids [n] int32 in (device), in any order;
  *   Y [n][dout] bf16 out = bf16_RN(X_t W'^T + s_a (X_t A_a^T) B_a^T), fp32
- *   accumulation, with bf16(s_a U_t) as the tensor cores' operand.  Up to 24
+ *   accumulation, with bf16(s_a U_t) as the tensor cores' operand.  Up to 32
  *   tokens may go by a weight stream, which does not round W' to bf16: it
  *   multiplies X with the book's entries as bf16 and scales each block's fp32
  *   partial sum by ahat.  Its Y is 2.5e-3 of the norm off the value on W', where

@@ -90,7 +90,11 @@ STREAM = [(4096, 4096, 1, 40, 16, "random", False, "int8"), (4096, 4096, 8, 40, 
           (8192, 28672, 8, 8, 16, "random", True, "plain"),                     # several epochs
           (1024, 11008, 12, 20, 64, "random", True, "int8"), (1024, 11008, 24, 40, 64, "random", False, "int8"),
           (16384, 1024, 24, 40, 64, "random", True, "int8"),                    # many pairs of a tile and an adapter
-          (4096, 4096, 24, 40, 128, "holes", True, "plain"), (4096, 4096, 16, 2, 40, "random", False, "e4m3")]
+          (4096, 4096, 24, 40, 128, "holes", True, "plain"), (4096, 4096, 16, 2, 40, "random", False, "e4m3"),
+          # rows that the GEMM's tiles do not divide
+          (4160, 4096, 9, 9, 16, "random", False, "int8"), (1088, 2048, 24, 40, 24, "holes", True, "e4m3"),
+          (4160, 4096, 32, 32, 64, "random", False, "int8"), (64, 4096, 25, 40, 128, "random", True, "plain"),
+          (11072, 4096, 30, 3, 16, "holes", True, "int8"), (192, 512, 32, 32, 8, "random", False, "int8")]
 # product rows (outputs), its depth, n, adapters, r, ids, ranks, weight: weight sub-tiles, token sub-tiles, K split
 GEMM = {(1024, 2048, 100, 9, 16, "random", True, "int8"): (1, 1, 4), (4096, 8192, 16, 9, 16, "random", True, "int8"): (1, 1, 4),
         (4096, 11008, 12, 6, 32, "holes", False, "e4m3"): (1, 1, 4), (1024, 4096, 32, 32, 16, "random", False, "plain"): (1, 1, 4),
@@ -155,7 +159,8 @@ def test_sizes_take_the_variants_they_are_for(tmp_path):
     assert not wrong, wrong
 
 
-NONFINITE = [(4096, 4096, 8, 16), (1024, 11008, 24, 64),                                         # the stream (forward)
+NONFINITE = [(4096, 4096, 8, 16), (1024, 11008, 24, 64), (1088, 2048, 32, 16),                   # the stream (forward)
+             (1088, 2048, 100, 24),                                                             # the register-level GEMM
              (1024, 2048, 100, 16), (4096, 4096, 333, 24), (8192, 512, 700, 24), (5120, 4096, 333, 16),
              (8192, 1024, 900, 40), (11008, 4096, 203, 32)]
 
