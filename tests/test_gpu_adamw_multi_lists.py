@@ -71,3 +71,29 @@ def test_captured_steps_of_a_long_list(eight):
         step(lb, at_b, *HYPER)
     torch.cuda.synchronize()
     _same(a, b)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_a_tensor_of_more_than_2_31_elements(eight):
+    """Its first and last elements and those around 2^31 get the bits that they get in tensors of their own."""
+    step = (api.adamw8_multi_step if eight else api.adamw_multi_step)
+    n, at = (1 << 31) + 777, torch.full((1,), 3, dtype=torch.int64, device="cuda")
+    spans = [(0, 5120), ((1 << 31) - 2560, 2560), (1 << 31, 777)]  # whole blocks of 256 but for the last
+    # all but the spans is zero: zero gradients and states of zero parameters leave zeros
+    whole = [torch.zeros(n, device="cuda") for _ in range(2)]
+    if eight:
+        whole += [torch.zeros(-(-n // k), dtype=d, device="cuda") for _ in range(2)
+                  for k, d in ((1, torch.float8_e4m3fn), (256, torch.float32))]
+    else:
+        whole += [torch.zeros(n, device="cuda") for _ in range(2)]
+    small = _tensors([k for _, k in spans], eight)
+    cut = lambda x, a, k: x[a // 256:a // 256 + -(-k // 256)] if len(x) < n else x[a:a + k]  # noqa: E731
+    for (a, k), t in zip(spans, small):
+        t[-1] = None
+        for x, y in zip(whole, t):
+            cut(x, a, k).copy_(y)
+    step(_list([whole + [None]], eight), at, *HYPER)
+    step(_list(small, eight), at, *HYPER)
+    for (a, k), t in zip(spans, small):
+        _same([[cut(x, a, k) for x in whole]], [t[:-1]])
+    assert not any(x[10240:20480].float().any() for x in whole)
