@@ -38,8 +38,10 @@
 // k-step.)  All MMAs keep one shape: only
 // then do they run in the order of their issue.  A zero times an infinity would
 // still be a NaN, so the decoders also replace what is not finite in the
-// factor's tile by zero, and the epilogue adds those products to their own
-// tokens one by one (a path that finite factors never take).  A k-step of
+// factor's tile by 1 with its sign, and the epilogue adds those products to
+// their own tokens one by one (a path that finite factors never take; what the 1
+// brings is nothing beside an infinity, and of its sign where s U is infinite
+// too, where a zero would make it NaN).  A k-step of
 // chunks costs about as much as a weight step; a prefill tile of packed
 // sequences has one or two.
 // A MULTI kernel reads its activations and weights before the kernel ahead of
@@ -705,11 +707,10 @@ nf4_tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                 };
                 auto odd = [&]() { return __hadd2(__hadd2(o0, o1), __hadd2(o2, o3)); };
                 auto is_odd = [](const __nv_bfloat162 &v) { return __hisnan(__low2bfloat16(v)) || __hisnan(__high2bfloat16(v)); };
-                auto clear = [](uint4 *q, int n) {  // the non-finite of n vectors of 8
-                    uint32_t *w = reinterpret_cast<uint32_t *>(q);
+                auto clear = [](uint4 *q, int n) {  // the non-finite of n vectors of 8: to 1 or -1
+                    uint16_t *w = reinterpret_cast<uint16_t *>(q);
                     for (int h = 0; h < 8 * n; ++h)
-                        if (((w[h >> 1] >> (16 * (h & 1))) & 0x7f80u) == 0x7f80u)
-                            w[h >> 1] &= (h & 1) ? 0x0000ffffu : 0xffff0000u;
+                        if ((w[h] & 0x7f80u) == 0x7f80u) w[h] = (uint16_t)((w[h] & 0x8000u) | 0x3f80u);
                 };
                 bool bad = false;
                 if (!TRANS) {

@@ -197,3 +197,26 @@ def test_factors_that_are_not_finite(g, trans):
         assert torch.equal(torch.isnan(got[tok, m]), torch.isnan(want))
         assert math.isnan(x) or torch.equal(got[tok, m].double(), want)
     assert torch.equal(got[~spoiled], clean[~spoiled])
+
+
+@pytest.mark.parametrize("g", NONFINITE, ids=_id)
+@pytest.mark.parametrize("trans", [False, True])
+def test_an_infinite_factor_times_an_infinite_product(g, trans):
+    """U = X A^T is infinite where A is, and so is its product with an infinity of B: with the sign of the two, not NaN
+    (and dX from G = dY B and A the same way)."""
+    M, K, n, r = g
+    c = Big(*((K, M) if trans else (M, K)), n, 3, r, "random", seed=4)
+    c.ids[:3] = torch.arange(3, dtype=torch.int32, device="cuda")
+    _, U = c.fwd()
+    down, up = (c.B.transpose(1, 2), c.A.transpose(1, 2)) if trans else (c.A, c.B)  # [count][r][K], [count][M][r]
+    x = c.dY if trans else c.X
+    tok = (c.ids == 1).nonzero()[:, 0]
+    x[tok, 9] = x[tok, 9].abs() + 1  # not zero, one sign
+    down[1, 2, 9] = -INF
+    up[1, 5, 2], up[1, M - 1, 2], up[1, 6, 2] = INF, -INF, 0
+    got = (c.bwd(U=U)[0] if trans else c.fwd()[0])[tok].double()
+    low = -INF * c.s[1].item()
+    want = low * up[1, :, 2].double().sign()
+    assert torch.equal(torch.isnan(got), torch.isnan(want).expand_as(got))
+    there = ~torch.isnan(want)
+    assert torch.equal(got[:, there], want[there].expand(len(tok), -1))
